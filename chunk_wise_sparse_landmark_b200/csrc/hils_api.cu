@@ -79,6 +79,7 @@ enum Op {
   kOpAttnDecode,
   kOpPrefillHost,
   kOpPrefillBwd,
+  kOpCache8,  // any operation on an 8-bit cache
   kOpNone
 };
 
@@ -98,6 +99,7 @@ const char* uncovered(const Shape& s, Op op) {
       case kOpScorePrefill: return score ? nullptr : "f32 prefill scoring: no kernel for d = 128 with G = 8";
       case kOpAttnDecode: return dec ? nullptr : "f32 decode attention needs d in {64, 128} and S in {32, 64}";
       case kOpPrefillBwd: return nullptr;
+      case kOpCache8: return dec ? nullptr : "f32 8-bit caches need d in {64, 128} and S in {32, 64}";
       case kOpPrefillHost:
         if (!summ) return "f32 summaries: no kernel for d = 32 with S = 64";
         return score ? nullptr : "f32 prefill scoring: no kernel for d = 128 with G = 8";
@@ -706,6 +708,157 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
   HILS_TRY(dev_ctx(&ctx));
   HILS_LAUNCH(launch_attn_decode(s, q, k_pool, v_pool, idx, s_sel, out, workspace, (cudaStream_t)stream, ctx, dv),
               "attn_decode_paged");
+  return HILS_OK;
+}
+
+// host checks of a cache's description: what its format needs
+static hils_status_t cache_view(const Shape& s, const hils_cache_t* c, CacheView* cv) {
+  if (!aligned16(c->k_pool) || !aligned16(c->v_pool))
+    return fail(HILS_ERR_INVALID_ARG, "cache: NULL or unaligned pool");
+  cv->k_pool = c->k_pool;
+  cv->v_pool = c->v_pool;
+  cv->format = c->format;
+  if (c->format == HILS_KV_NATIVE) {
+    if (c->k_scale || c->v_scale || c->k_tail || c->v_tail)
+      return fail(HILS_ERR_INVALID_ARG, "cache: a native cache has no scales and no tails");
+    return HILS_OK;
+  }
+  if (!aligned16(c->k_scale) || !aligned16(c->v_scale) || !aligned16(c->k_tail) || !aligned16(c->v_tail))
+    return fail(HILS_ERR_INVALID_ARG, "cache: an 8-bit cache needs scales and tails (16-byte aligned)");
+  cv->k_scale = c->k_scale;
+  cv->v_scale = c->v_scale;
+  cv->k_tail = c->k_tail;
+  cv->v_tail = c->v_tail;
+  return HILS_OK;
+}
+
+// the shape, page table and cache of a hils_*_cache* call; `native` is the
+// operation whose shapes a native cache has
+static hils_status_t cache_args(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
+                                Op native, Shape* s, DecView* dv, CacheView* cv) {
+  if (!cache) return fail(HILS_ERR_INVALID_ARG, "cache description is NULL");
+  if (cache->format != HILS_KV_NATIVE && cache->format != HILS_KV_I8 && cache->format != HILS_KV_E4M3)
+    return fail(HILS_ERR_INVALID_ARG, "cache: unknown format %d", cache->format);
+  HILS_TRY(make_shape(cfg, s, cache->format == HILS_KV_NATIVE ? native : kOpCache8));
+  HILS_TRY(paged_view(*s, paged, dv));
+  return cache_view(*s, cache, cv);
+}
+
+hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
+                                const hils_rows_t* rows, const hils_rope_t* rope, void* stream) {
+  HILS_NVTX;
+  Shape s;
+  DecView dv;
+  CacheView cv;
+  HILS_TRY(cache_args(cfg, paged, cache, kOpSummaries, &s, &dv, &cv));
+  if (!rows) return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: rows is NULL");
+  if (rows->n_rows < 0) return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: n_rows %d < 0", rows->n_rows);
+  if (!rows->row_start && rows->n_rows != s.B)
+    return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: without row_start n_rows must be B (%d, got %d)", s.B,
+                rows->n_rows);
+  if (((uintptr_t)rows->row_start | (uintptr_t)rows->positions) & 3u)
+    return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: unaligned row_start or positions");
+  if (rows->n_rows > 0) {
+    if (!aligned16(rows->k) || !aligned16(rows->v) || (rows->q && (!aligned16(rows->q) || !aligned16(rows->q_out))))
+      return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: NULL or unaligned pointer");
+    const int64_t per16 = 16 / (int64_t)esize(s);
+    const int64_t st[8] = {rows->k_row, rows->k_head, rows->v_row,     rows->v_head,
+                           rows->q_row, rows->q_head, rows->q_out_row, rows->q_out_head};
+    for (int i = 0; i < (rows->q ? 8 : 4); ++i)
+      if (st[i] < 0 || st[i] % per16)
+        return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: a stride of %lld elements is negative or no multiple of "
+                                          "16 bytes",
+                    (long long)st[i]);
+    if (rows->q == rows->q_out && rows->q && (st[4] != st[6] || st[5] != st[7]))
+      return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: q_out in place needs the strides of q");
+  }
+  RopeView rp;
+  if (rope) {
+    if (!aligned16(rope->cos_table) || !aligned16(rope->sin_table))
+      return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: NULL or unaligned angle table");
+    if (rope->max_pos < 1 || rope->rot_dim < 16 || rope->rot_dim % 16 || rope->rot_dim > s.d ||
+        (rope->interleaved != 0 && rope->interleaved != 1))
+      return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: rope needs max_pos >= 1, rot_dim a multiple of 16 up to "
+                                        "d, interleaved 0 or 1 (max_pos=%d rot_dim=%d interleaved=%d)",
+                  rope->max_pos, rope->rot_dim, rope->interleaved);
+    rp.cos_t = rope->cos_table;
+    rp.sin_t = rope->sin_table;
+    rp.max_pos = rope->max_pos;
+    rp.rot = rope->rot_dim;
+    rp.interleaved = rope->interleaved;
+  }
+  if (rows->n_rows == 0) return HILS_OK;
+  NewRows nr{rows->k,      rows->v,      rows->q,     rows->q_out, rows->k_row,     rows->k_head,     rows->v_row,
+             rows->v_head, rows->q_row,  rows->q_head, rows->q_out_row, rows->q_out_head, rows->row_start,
+             rows->positions, rows->n_rows};
+  DevCtx ctx;
+  HILS_TRY(dev_ctx(&ctx));
+  HILS_LAUNCH(launch_cache_append(s, cv, dv, nr, rp, (cudaStream_t)stream, ctx), "cache_append");
+  return HILS_OK;
+}
+
+hils_status_t hils_build_summaries_cache(const hils_config_t* cfg, const hils_paged_t* paged,
+                                         const hils_cache_t* cache, const void* q_lmk, int32_t lmk,
+                                         const int32_t* from_lens, void* k_sum, float* b_sum, void* stream) {
+  HILS_NVTX;
+  Shape s;
+  DecView dv;
+  CacheView cv;
+  HILS_TRY(cache_args(cfg, paged, cache, kOpSummaries, &s, &dv, &cv));
+  if (!aligned16(q_lmk) || !aligned16(k_sum) || !aligned16(b_sum) || ((uintptr_t)from_lens & 3u))
+    return fail(HILS_ERR_INVALID_ARG, "hils_build_summaries_cache: NULL or unaligned pointer");
+  const long long d = s.d;
+  LmkStrides ls;
+  switch (lmk) {
+    case HILS_LMK_CHUNK: ls = LmkStrides{s.Hq * (s.C * d), s.C * d, d}; break;
+    case HILS_LMK_SEQUENCE: ls = LmkStrides{s.Hq * d, d, 0}; break;
+    case HILS_LMK_SHARED: ls = LmkStrides{0, d, 0}; break;
+    default: return fail(HILS_ERR_INVALID_ARG, "hils_build_summaries_cache: unknown landmark layout %d", lmk);
+  }
+  DevCtx ctx;
+  HILS_TRY(dev_ctx(&ctx));
+  HILS_LAUNCH(launch_summaries_cache(s, cv, dv, q_lmk, ls, from_lens, k_sum, b_sum, (cudaStream_t)stream, ctx),
+              "summaries_cache");
+  return HILS_OK;
+}
+
+hils_status_t hils_attn_decode_cache(const hils_config_t* cfg, const void* q, const hils_paged_t* paged,
+                                     const hils_cache_t* cache, const int32_t* idx, const float* s_sel, void* out,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  if (cache && cache->format == HILS_KV_NATIVE) {
+    Shape s;
+    DecView dv;
+    CacheView cv;
+    HILS_TRY(cache_args(cfg, paged, cache, kOpAttnDecode, &s, &dv, &cv));
+    return hils_attn_decode_paged(cfg, q, cache->k_pool, cache->v_pool, paged, idx, s_sel, out, workspace, ws_bytes,
+                                  stream);
+  }
+  HILS_NVTX;
+  Shape s;
+  DecView dv;
+  CacheView cv;
+  HILS_TRY(cache_args(cfg, paged, cache, kOpAttnDecode, &s, &dv, &cv));
+  if (!aligned16(q) || !aligned16(idx) || !aligned16(s_sel) || !aligned16(out))
+    return fail(HILS_ERR_INVALID_ARG, "hils_attn_decode_cache: NULL or unaligned pointer");
+  DevCtx ctx;
+  HILS_TRY(dev_ctx(&ctx));
+  HILS_LAUNCH(launch_attn_codes(s, q, cv, dv, idx, s_sel, out, (cudaStream_t)stream, ctx), "attn_decode_cache");
+  return HILS_OK;
+}
+
+hils_status_t hils_cache_read(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
+                              void* k_out, void* v_out, int32_t out_rows, void* stream) {
+  HILS_NVTX;
+  Shape s;
+  DecView dv;
+  CacheView cv;
+  HILS_TRY(cache_args(cfg, paged, cache, kOpSummaries, &s, &dv, &cv));
+  if ((!k_out && !v_out) || (k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)))
+    return fail(HILS_ERR_INVALID_ARG, "hils_cache_read: no output, or an unaligned one");
+  if (out_rows < 1) return fail(HILS_ERR_INVALID_ARG, "hils_cache_read: out_rows %d < 1", out_rows);
+  DevCtx ctx;
+  HILS_TRY(dev_ctx(&ctx));
+  HILS_LAUNCH(launch_cache_read(s, cv, dv, k_out, v_out, out_rows, (cudaStream_t)stream, ctx), "cache_read");
   return HILS_OK;
 }
 

@@ -18,6 +18,15 @@ struct Shape {
   int dtype;  // 0 f32, 1 bf16
 };
 
+// Element offset of the landmark query of (sequence b, query head h, chunk c):
+// per-chunk queries use strides (Hq C d, C d, d), a decode step's one query per
+// head and sequence (Hq d, d, 0), the landmark-free variant's one shared query
+// per head (0, d, 0).
+struct LmkStrides {
+  long long b, h, c;
+  HILS_DI long long of(int bb, int hh, int cc) const { return bb * b + hh * h + cc * c; }
+};
+
 // The decode cache as the decode kernels see it.  Default: every sequence has
 // length N and its keys and values are contiguous [B, Hkv, N, d].  Paged: a
 // pool of one-chunk pages [num_pages, Hkv, S, d]; chunk c of sequence b lives
@@ -39,6 +48,51 @@ HILS_DI long long dv_chunk(const DecView& v, const Shape& s, int b, int g, int c
   if (p < 0 || p >= v.num_pages) return -1;
   return ((long long)p * s.Hkv + g) * s.S * s.d;
 }
+
+// A paged cache of any format (kNative: the shape's type; kI8, kE4M3: one byte
+// an element, one scale for each page and KV head, incomplete chunks in the
+// tails [B, 2, Hkv, S, d], chunk c in slot c & 1).
+enum KvFormat : int { kNative = 0, kI8 = 1, kE4M3 = 2 };
+struct CacheView {
+  void* k_pool = nullptr;
+  void* v_pool = nullptr;
+  float* k_scale = nullptr;
+  float* v_scale = nullptr;
+  void* k_tail = nullptr;
+  void* v_tail = nullptr;
+  int format = kNative;
+};
+// the largest magnitude of a code
+HILS_DI float max_code(int format) { return format == kI8 ? 127.f : 448.f; }
+// element offset of chunk c's tile in a tail
+HILS_DI long long tail_off(const Shape& s, int b, int g, int c) {
+  return (((long long)b * 2 + (c & 1)) * s.Hkv + g) * s.S * s.d;
+}
+// the new rows of an append (strides in elements) and the angle tables
+struct NewRows {
+  const void *k, *v, *q;
+  void* q_out;
+  long long k_row, k_head, v_row, v_head, q_row, q_head, q_out_row, q_out_head;
+  const int* row_start;
+  const int* positions;
+  int n_rows;
+};
+struct RopeView {
+  const float* cos_t = nullptr;
+  const float* sin_t = nullptr;
+  int max_pos = 0, rot = 0, interleaved = 0;
+};
+cudaError_t launch_cache_append(const Shape& s, const CacheView& cv, const DecView& dv, const NewRows& rows,
+                                const RopeView& rope, cudaStream_t st, const DevCtx& ctx);
+cudaError_t launch_cache_read(const Shape& s, const CacheView& cv, const DecView& dv, void* k_out, void* v_out,
+                              int out_rows, cudaStream_t st, const DevCtx& ctx);
+// summaries of chunks [from[b] / S, len[b] / S) over a cache of any format
+// (lmk: strides of the landmark queries), and decode attention over an 8-bit one
+cudaError_t launch_summaries_cache(const Shape& s, const CacheView& cv, const DecView& dv, const void* q_lmk,
+                                   const LmkStrides& lmk, const int* from, void* k_sum, float* b_sum,
+                                   cudaStream_t st, const DevCtx& ctx);
+cudaError_t launch_attn_codes(const Shape& s, const void* q, const CacheView& cv, const DecView& dv,
+                              const int32_t* idx, const float* s_sel, void* out, cudaStream_t st, const DevCtx& ctx);
 
 // K1: landmark summaries (all dtypes); shared_lmk: q_lmk is one query per head
 // [Hq, d] shared by every chunk and sequence (the landmark-free variant)

@@ -20,14 +20,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Element offset of the landmark query of (sequence b, query head h, chunk c):
-// per-chunk queries use strides (Hq C d, C d, d); the landmark-free variant's
-// one shared query per head uses (0, d, 0).
-struct LmkStrides {
-  long long b, h, c;
-  HILS_DI long long of(int bb, int hh, int cc) const { return bb * b + hh * h + cc * c; }
-};
-
 // Which chunks a launch summarises.  kAllChunks: every complete chunk of a
 // contiguous cache [B, Hkv, N, d].  kPagedAll: every complete chunk of each
 // sequence of a paged cache (units over max_pages, those past the sequence's

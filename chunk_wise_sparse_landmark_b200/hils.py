@@ -19,6 +19,8 @@ HILS_OK, HILS_ERR_INVALID_ARG, HILS_ERR_UNSUPPORTED, HILS_ERR_CUDA, HILS_ERR_TIM
 HILS_F32, HILS_BF16 = 0, 1
 (HILS_WS_SCORE_PREFILL, HILS_WS_SCORE_DECODE, HILS_WS_ATTN_DECODE, HILS_WS_PREFILL_HOST, HILS_WS_ATTN_PREFILL,
  HILS_WS_PREFILL_BWD) = range(6)
+HILS_KV_NATIVE, HILS_KV_I8, HILS_KV_E4M3 = range(3)
+HILS_LMK_CHUNK, HILS_LMK_SEQUENCE, HILS_LMK_SHARED = range(3)
 
 EXPORTS = (
     "hils_build_summaries",
@@ -33,6 +35,10 @@ EXPORTS = (
     "hils_build_summaries_paged",
     "hils_score_topk_paged",
     "hils_attn_decode_paged",
+    "hils_cache_append",
+    "hils_build_summaries_cache",
+    "hils_attn_decode_cache",
+    "hils_cache_read",
     "hils_host_device_pointer",
     "hils_workspace_bytes",
     "hils_sync_status",
@@ -85,6 +91,51 @@ class Paged(ctypes.Structure):
     ]
 
 
+class Cache(ctypes.Structure):
+    """A paged cache of any format (include/hils.h, hils_cache_t)."""
+    _fields_ = [
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("k_tail", ctypes.c_void_p),
+        ("v_tail", ctypes.c_void_p),
+        ("format", ctypes.c_int32),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """The new rows of an append (include/hils.h, hils_rows_t)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_row", ctypes.c_int64),
+        ("k_head", ctypes.c_int64),
+        ("v_row", ctypes.c_int64),
+        ("v_head", ctypes.c_int64),
+        ("q_row", ctypes.c_int64),
+        ("q_head", ctypes.c_int64),
+        ("q_out_row", ctypes.c_int64),
+        ("q_out_head", ctypes.c_int64),
+        ("row_start", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
+    ]
+
+
+class Rope(ctypes.Structure):
+    """Angle tables of the rotary position embedding (include/hils.h, hils_rope_t)."""
+    _fields_ = [
+        ("cos_table", ctypes.c_void_p),
+        ("sin_table", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -111,6 +162,11 @@ def load() -> ctypes.CDLL:
         lib.hils_build_summaries_paged.argtypes = [C, PG, P, P, P, P, P]
         lib.hils_score_topk_paged.argtypes = [C, P, PG, P, P, P, P, P, ctypes.c_size_t, P]
         lib.hils_attn_decode_paged.argtypes = [C, P, P, P, PG, P, P, P, P, ctypes.c_size_t, P]
+        CA = ctypes.POINTER(Cache)
+        lib.hils_cache_append.argtypes = [C, PG, CA, ctypes.POINTER(Rows), ctypes.POINTER(Rope), P]
+        lib.hils_build_summaries_cache.argtypes = [C, PG, CA, P, ctypes.c_int32, P, P, P, P]
+        lib.hils_attn_decode_cache.argtypes = [C, P, PG, CA, P, P, P, P, ctypes.c_size_t, P]
+        lib.hils_cache_read.argtypes = [C, PG, CA, P, P, ctypes.c_int32, P]
         lib.hils_workspace_bytes.argtypes = [C, ctypes.c_int32, ctypes.c_int32]
         lib.hils_workspace_bytes.restype = ctypes.c_size_t
         lib.hils_sync_status.argtypes = [P]
@@ -123,7 +179,8 @@ def load() -> ctypes.CDLL:
         for n in ("hils_build_summaries", "hils_build_summaries_shared", "hils_score_topk", "hils_attn_prefill",
                   "hils_attn_decode", "hils_attn_decode_noalloc", "hils_prefill_host", "hils_prefill_bwd",
                   "hils_decode_append", "hils_build_summaries_paged", "hils_score_topk_paged",
-                  "hils_attn_decode_paged", "hils_sync_status"):
+                  "hils_attn_decode_paged", "hils_cache_append", "hils_build_summaries_cache",
+                  "hils_attn_decode_cache", "hils_cache_read", "hils_sync_status"):
             getattr(lib, n).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -206,7 +263,9 @@ def hils_prefill_bwd(cfg: Config, q, k, v, q_lmk, idx, s_sel, k_sum, dout, dq, d
 def paged(seq_lens, block_table, num_pages: int) -> Paged:
     """seq_lens [B] and block_table [B, max_pages] are int32 CUDA tensors."""
     assert seq_lens.dtype == torch.int32 and block_table.dtype == torch.int32
-    return Paged(_p(seq_lens).value, _p(block_table).value, block_table.shape[1], num_pages)
+    pg = Paged(_p(seq_lens).value, _p(block_table).value, block_table.shape[1], num_pages)
+    pg.tensors = (seq_lens, block_table)  # the description keeps what it points to
+    return pg
 
 
 def hils_decode_append(cfg: Config, pg: Paged, k_new, v_new, q_lmk_new, k_pool, v_pool, k_sum, b_sum, stream=None):
@@ -229,6 +288,153 @@ def hils_attn_decode_paged(cfg: Config, q, k_pool, v_pool, pg: Paged, idx, s_sel
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().hils_attn_decode_paged(ctypes.byref(cfg), _p(q), _p(k_pool), _p(v_pool), ctypes.byref(pg), _p(idx),
                                          _p(s_sel), _p(out), _p(workspace), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------ caches of any format ---
+
+def _dtype(cfg: Config):
+    return torch.float32 if cfg.dtype == HILS_F32 else torch.bfloat16
+
+
+def _t(t: torch.Tensor, shape, dtype, device) -> int:
+    """Address of a contiguous tensor that must have this shape, type and device."""
+    assert t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous(), (
+        f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, heads: int, cfg: Config, n: int, device) -> int:
+    """Address of rows [n, heads, d] whose heads are contiguous (any row and head strides)."""
+    assert t.shape == (n, heads, cfg.head_dim) and t.dtype is _dtype(cfg) and t.device == device, (
+        f"expected {_dtype(cfg)} rows [{n}, {heads}, {cfg.head_dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    assert t.stride(2) == 1, "the elements of a head must be contiguous"
+    return t.data_ptr()
+
+
+def _launch(device, fn, *args, stream):
+    """fn(*args, stream) on the tensors' device (its current stream if None)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
+    else:
+        _check(fn(*args, stream.cuda_stream))
+
+
+def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) -> Cache:
+    """A paged cache.  Pools [num_pages, Hkv, S, d] of float32 / bfloat16 (native), int8 or
+    float8_e4m3fn (8 bits: with float32 scales [num_pages, Hkv] and tails [B, 2, Hkv, S, d])."""
+    fmt = {torch.float32: HILS_KV_NATIVE, torch.bfloat16: HILS_KV_NATIVE, torch.int8: HILS_KV_I8,
+           torch.float8_e4m3fn: HILS_KV_E4M3}.get(k_pool.dtype)
+    assert fmt is not None and k_pool.ndim == 4, "pools are [num_pages, Hkv, S, d] of float32, bfloat16, int8 or float8_e4m3fn"
+    dev, (pages, hkv, S, d) = k_pool.device, k_pool.shape
+    c = Cache(_t(k_pool, k_pool.shape, k_pool.dtype, dev), _t(v_pool, k_pool.shape, k_pool.dtype, dev), None, None,
+              None, None, fmt)
+    c.elements = k_pool.dtype
+    if fmt != HILS_KV_NATIVE:
+        assert k_scale is not None and v_scale is not None and k_tail is not None and v_tail is not None, (
+            "an 8-bit cache needs scales and tails")
+        c.k_scale, c.v_scale = (_t(x, (pages, hkv), torch.float32, dev) for x in (k_scale, v_scale))
+        assert k_tail.dtype in (torch.float32, torch.bfloat16)
+        tail = (k_tail.shape[0], 2, hkv, S, d)
+        c.k_tail, c.v_tail = (_t(x, tail, k_tail.dtype, dev) for x in (k_tail, v_tail))
+        c.elements = k_tail.dtype
+        c.sequences = k_tail.shape[0]
+    else:
+        assert k_scale is None and v_scale is None and k_tail is None and v_tail is None, (
+            "a native cache has no scales and no tails")
+        c.sequences = None
+    c.device, c.tile, c.pages = dev, (hkv, S, d), pages
+    c.tensors = (k_pool, v_pool, k_scale, v_scale, k_tail, v_tail)
+    return c
+
+
+def _cache_fits(cfg: Config, pg: Paged, c: Cache):
+    assert c.tile == (cfg.n_kv_heads, cfg.chunk, cfg.head_dim) and c.elements is _dtype(cfg) and (
+        pg.num_pages <= c.pages and c.sequences in (None, cfg.batch)), "the cache does not fit the configuration or its page table"
+
+
+def rope(cos, sin, interleaved: bool = False) -> Rope:
+    """Angle tables: float32 cos and sin [max_pos, rot_dim / 2]; pairs (x[i], x[i + rot_dim / 2]),
+    or (x[2i], x[2i + 1]) if interleaved."""
+    assert cos.ndim == 2 and cos.is_cuda
+    r = Rope(_t(cos, cos.shape, torch.float32, cos.device), _t(sin, cos.shape, torch.float32, cos.device), cos.shape[0],
+             2 * cos.shape[1], int(interleaved))
+    r.device = cos.device
+    r.tensors = (cos, sin)
+    return r
+
+
+def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """cos and sin of p base^(-2 i / rot_dim), computed in float64, as float32 [max_pos, rot_dim / 2]."""
+    i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * base ** (-2 * i / rot_dim)
+    return angle.cos().float(), angle.sin().float()
+
+
+def hils_cache_append(cfg: Config, pg: Paged, cache: Cache, k, v, q=None, q_out=None, rope: Rope | None = None,
+                      row_start=None, positions=None, stream=None):
+    """Rotate and append: k, v [n, Hkv, d], q and q_out [n, Hq, d] (views with contiguous heads);
+    row_start [B + 1] and positions [n] int32."""
+    _cache_fits(cfg, pg, cache)
+    dev, n, hkv = cache.device, k.shape[0], cfg.n_kv_heads
+    r = Rows(_rows(k, hkv, cfg, n, dev), _rows(v, hkv, cfg, n, dev), None, None, k.stride(0), k.stride(1),
+             v.stride(0), v.stride(1), 0, 0, 0, 0, None, None, n)
+    if q is not None:
+        assert q_out is not None, "q needs q_out"
+        r.q, r.q_out = _rows(q, cfg.n_q_heads, cfg, n, dev), _rows(q_out, cfg.n_q_heads, cfg, n, dev)
+        r.q_row, r.q_head = q.stride(0), q.stride(1)
+        r.q_out_row, r.q_out_head = q_out.stride(0), q_out.stride(1)
+    if row_start is not None:
+        r.row_start = _t(row_start, (cfg.batch + 1,), torch.int32, dev)
+    if positions is not None:
+        r.positions = _t(positions, (n,), torch.int32, dev)
+    if rope is not None:
+        assert rope.device == dev, "the angle tables are on another device than the cache"
+        rope = ctypes.byref(rope)
+    _launch(dev, load().hils_cache_append, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache), ctypes.byref(r),
+            rope, stream=stream)
+
+
+def hils_build_summaries_cache(cfg: Config, pg: Paged, cache: Cache, q_lmk, k_sum, b_sum, from_lens=None, stream=None):
+    """Summaries over a cache of any format; q_lmk [B, Hq, C, d], one for each sequence
+    [B, Hq, d], or one for all [Hq, d]; from_lens [B] int32: only chunks completed since."""
+    _cache_fits(cfg, pg, cache)
+    dev, B, hq, d = cache.device, cfg.batch, cfg.n_q_heads, cfg.head_dim
+    C = cfg.seq_len // cfg.chunk
+    lmk, shape = {4: (HILS_LMK_CHUNK, (B, hq, C, d)), 3: (HILS_LMK_SEQUENCE, (B, hq, d)),
+                  2: (HILS_LMK_SHARED, (hq, d))}[q_lmk.ndim]
+    el = cache.elements
+    _launch(dev, load().hils_build_summaries_cache, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache),
+            _t(q_lmk, shape, el, dev), lmk, None if from_lens is None else _t(from_lens, (B,), torch.int32, dev),
+            _t(k_sum, (B, hq, C, d), el, dev), _t(b_sum, (B, hq, C), torch.float32, dev), stream=stream)
+
+
+def hils_attn_decode_cache(cfg: Config, q, pg: Paged, cache: Cache, idx, s_sel, out, workspace=None, stream=None):
+    """Decode attention over a cache of any format (workspace: native caches only)."""
+    _cache_fits(cfg, pg, cache)
+    dev, B, hq, K, el = cache.device, cfg.batch, cfg.n_q_heads, cfg.top_k, cache.elements
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        assert workspace.device == dev and workspace.is_contiguous()
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    row = (B, hq, cfg.head_dim)
+    _launch(dev, load().hils_attn_decode_cache, ctypes.byref(cfg), _t(q, row, el, dev), ctypes.byref(pg),
+            ctypes.byref(cache), _t(idx, (B, cfg.n_kv_heads, K), torch.int32, dev),
+            _t(s_sel, (B, hq, K), torch.float32, dev), _t(out, row, el, dev), ws, ws_bytes, stream=stream)
+
+
+def hils_cache_read(cfg: Config, pg: Paged, cache: Cache, k_out=None, v_out=None, stream=None):
+    """The cache's values as rows k_out, v_out [B, Hkv, rows, d]; rows behind a sequence are left as they were."""
+    _cache_fits(cfg, pg, cache)
+    some = k_out if k_out is not None else v_out
+    assert some is not None and some.ndim == 4, "k_out or v_out [B, Hkv, rows, d] is needed"
+    shape = (cfg.batch, cfg.n_kv_heads, some.shape[2], cfg.head_dim)
+    k, v = (None if t is None else _t(t, shape, cache.elements, cache.device) for t in (k_out, v_out))
+    _launch(cache.device, load().hils_cache_read, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache), k, v,
+            some.shape[2], stream=stream)
 
 
 def _ph(t: torch.Tensor):
@@ -345,4 +551,54 @@ class Decode:
     def step(self, q, k_cache, v_cache, stream=None):
         hils_score_topk(self.cfg, q, self.k_sum, self.b_sum, self.idx, self.s_sel, self.ws_score, True, None, stream)
         hils_attn_decode(self.cfg, q, k_cache, v_cache, self.idx, self.s_sel, self.out, self.ws_attn, stream)
+        return self.out
+
+
+class CacheDecode:
+    """Buffers and calls for decoding on a paged cache of any format.
+
+    fmt: "native", "int8" or "e4m3".  The caller owns the page table and the
+    lengths (int32 CUDA tensors): block_table [B, >= ceil(seq_len / S)] names
+    the pool's pages, seq_lens [B] counts the tokens of each sequence with
+    those being appended.  A step of a layer is :meth:`append` (rotation,
+    cache, summaries of the chunks it completes) and :meth:`step` (scores,
+    selection, attention)."""
+
+    _POOL = {"native": None, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+    def __init__(self, cfg: Config, seq_lens, block_table, num_pages: int, fmt: str = "int8", rope: Rope | None = None):
+        self.cfg, self.rope, self.device = cfg, rope, seq_lens.device
+        B, Hq, Hkv, d, S, K = cfg.batch, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.chunk, cfg.top_k
+        dt, dev = _dtype(cfg), self.device
+        C = cfg.seq_len // S
+        assert seq_lens.shape == (B,) and block_table.shape[0] == B
+        self.seq_lens, self.block_table = seq_lens, block_table
+        self.paged = paged(seq_lens, block_table, num_pages)
+        el = self._POOL[fmt] or dt
+        pools = [torch.zeros((num_pages, Hkv, S, d), dtype=el, device=dev) for _ in range(2)]
+        rest = []
+        if el is not dt:
+            rest = [torch.zeros((num_pages, Hkv), dtype=torch.float32, device=dev) for _ in range(2)]
+            rest += [torch.zeros((B, 2, Hkv, S, d), dtype=dt, device=dev) for _ in range(2)]
+        self.cache = cache(*pools, *rest)
+        self.k_sum = torch.zeros((B, Hq, C, d), dtype=dt, device=dev)
+        self.b_sum = torch.zeros((B, Hq, C), dtype=torch.float32, device=dev)
+        self.idx = torch.empty((B, Hkv, K), dtype=torch.int32, device=dev)
+        self.s_sel = torch.empty((B, Hq, K), dtype=torch.float32, device=dev)
+        self.out = torch.empty((B, Hq, d), dtype=dt, device=dev)
+        self.ws_score = alloc_workspace(workspace_bytes(cfg, HILS_WS_SCORE_DECODE), dev)
+        self.ws_attn = None if rest else alloc_workspace(workspace_bytes(cfg, HILS_WS_ATTN_DECODE), dev)
+
+    def append(self, k, v, q_lmk, q=None, q_out=None, row_start=None, from_lens=None, positions=None, stream=None):
+        """Rows k, v [n, Hkv, d] (and q -> q_out [n, Hq, d]) of the new tokens, then the summaries of the
+        chunks from position from_lens[b] on (all if None) that are complete, by q_lmk
+        (:func:`hils_build_summaries_cache`)."""
+        hils_cache_append(self.cfg, self.paged, self.cache, k, v, q, q_out, self.rope, row_start, positions, stream)
+        hils_build_summaries_cache(self.cfg, self.paged, self.cache, q_lmk, self.k_sum, self.b_sum, from_lens, stream)
+        return q_out
+
+    def step(self, q, stream=None):
+        """Attention of q [B, Hq, d], each sequence's last token (rotated)."""
+        hils_score_topk_paged(self.cfg, q, self.paged, self.k_sum, self.b_sum, self.idx, self.s_sel, self.ws_score, stream)
+        hils_attn_decode_cache(self.cfg, q, self.paged, self.cache, self.idx, self.s_sel, self.out, self.ws_attn, stream)
         return self.out

@@ -278,6 +278,124 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
                                      void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * A paged decode cache in the configuration's type or in 8 bits, filled by
+ * hils_cache_append.  The pages have no counterpart: [Exp] counts the bytes
+ * that a decode step touches, and codes of one byte halve them (and the pool).
+ *
+ * Layout: chunk c of sequence b is page block_table[b * max_pages + c] of
+ * k_pool / v_pool [num_pages, Hkv, S, d] (hils_paged_t).  format:
+ *   HILS_KV_NATIVE  elements of cfg->dtype; the other pointers are NULL.
+ *   HILS_KV_I8      signed bytes;     value = code * scale (float32)
+ *   HILS_KV_E4M3    8-bit e4m3 codes; value = code * scale (float32)
+ * with one scale for each page and KV head, k_scale / v_scale [num_pages,
+ * Hkv] (a block of S tokens and one head).  A block X of S x d values of
+ * cfg->dtype with largest magnitude A is held as
+ *   scale = A / M,  code = round_to_nearest_even(x * (M / A)),  M = 127 or 448
+ * (float32 operations).  A block with A < 2^-110 is held as zeros (scale 0);
+ * a block with an infinity or a NaN gets the scale NaN, so that whatever
+ * reads it is NaN.
+ *   A chunk becomes codes when its last token arrives.  Until then its tokens
+ * are in the tails k_tail / v_tail [B, 2, Hkv, S, d] (cfg->dtype), chunk c in
+ * slot c & 1; hils_cache_append also writes the new tokens of the chunk
+ * before the last one there.  So what the cache holds does not depend on how
+ * the tokens were split over calls, and a sequence may be cut back by the
+ * tokens of its last chunk and the one before (its length reduced, other
+ * tokens appended) as long as every token of those two chunks was appended
+ * here.  8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
+ * and dtype BF16 with d = 128, S = 64; native caches every shape of the
+ * summaries (hils_attn_decode_cache: those of hils_attn_decode_paged).
+ * Pools, tails and scales are 16-byte aligned.
+ */
+typedef enum { HILS_KV_NATIVE = 0, HILS_KV_I8 = 1, HILS_KV_E4M3 = 2 } hils_kv_format_t;
+
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  void* k_tail;
+  void* v_tail;
+  int32_t format; /* hils_kv_format_t */
+} hils_cache_t;
+
+/* Rotary position embedding.  Pair i < rot_dim / 2 of a head's row x at
+ * position p: (x[i], x[i + rot_dim / 2]), or (x[2i], x[2i + 1]) if
+ * interleaved, is turned by the angle of row p of the tables:
+ *   (a, c) -> (a cos - c sin, c cos + a sin)
+ * in float32, each product rounded by itself, the result rounded once to
+ * cfg->dtype.  Elements from rot_dim on stay as they are. */
+typedef struct {
+  const float* cos_table; /* [max_pos, rot_dim / 2] device, 16-byte aligned */
+  const float* sin_table; /* [max_pos, rot_dim / 2] */
+  int32_t max_pos;
+  int32_t rot_dim;        /* a multiple of 16, 16 <= rot_dim <= d */
+  int32_t interleaved;    /* 0 or 1 */
+} hils_rope_t;
+
+/* The new tokens of one append: n_rows rows, those of sequence b at rows
+ * [row_start[b], row_start[b + 1]) in the order of their positions, the last
+ * at position seq_lens[b] - 1.  A sequence may have none.  Strides are in
+ * elements, from one row / one head to the next (multiples of 16 bytes; the d
+ * elements of a head are contiguous), so that k, v and q may be views of one
+ * projection's output.  q may be NULL; else its rotated rows go to q_out, which
+ * may be q itself with the same strides and overlaps nothing otherwise. */
+typedef struct {
+  const void* k;            /* [n_rows, Hkv, d] dtype */
+  const void* v;            /* [n_rows, Hkv, d] */
+  const void* q;            /* [n_rows, Hq, d] or NULL */
+  void* q_out;              /* [n_rows, Hq, d] */
+  int64_t k_row, k_head, v_row, v_head, q_row, q_head, q_out_row, q_out_head;
+  const int32_t* row_start; /* [B + 1] device; NULL: n_rows = B, one row for each sequence */
+  const int32_t* positions; /* [n_rows] device: rows of the angle tables; NULL: the cache positions */
+  int32_t n_rows;
+} hils_rows_t;
+
+/* Rotates the new tokens' keys (and queries) and appends keys and values to
+ * the cache (one launch; paged->seq_lens already counts the new tokens).
+ *   rope: NULL leaves q and k as they are (q is then copied to q_out).
+ * Checked on the device and reported as for hils_decode_append: a sequence
+ * with new rows whose rows do not lie in [0, n_rows) in order, whose length is
+ * outside [1, L_max] or below its number of new rows is skipped; a page outside
+ * the pool is not written; a row whose position lies outside the tables is
+ * stored unrotated.  Rows of no sequence (before row_start[0], from
+ * row_start[B] on) are neither read nor written.  No page may belong to two
+ * chunks that one call writes.  The value rows, scales and codes repeat bit
+ * for bit. */
+hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
+                                const hils_rows_t* rows, const hils_rope_t* rope, void* stream);
+
+/* Landmark queries of hils_build_summaries_cache: one for each chunk
+ * [B, Hq, C, d], one for each sequence [B, Hq, d] (a decode step's, for the
+ * chunk that its token completes), or one for all [Hq, d] (landmark-free). */
+typedef enum { HILS_LMK_CHUNK = 0, HILS_LMK_SEQUENCE = 1, HILS_LMK_SHARED = 2 } hils_lmk_t;
+
+/* hils_build_summaries_paged over a cache of any format (k = code * scale):
+ * the summaries of the complete chunks of each sequence, or with from_lens
+ * ([B] device, or NULL) of those that its tokens from position from_lens[b] on
+ * completed: chunks [from_lens[b] / S, seq_lens[b] / S).  Entries of other
+ * chunks of k_sum and b_sum are left as they were.  lmk: hils_lmk_t. */
+hils_status_t hils_build_summaries_cache(const hils_config_t* cfg, const hils_paged_t* paged,
+                                         const hils_cache_t* cache, const void* q_lmk, int32_t lmk,
+                                         const int32_t* from_lens, void* k_sum, float* b_sum, void* stream);
+
+/* hils_attn_decode_paged over a cache of any format: selected chunks and the
+ * window's complete chunks from the pool, the incomplete chunk from the tail.
+ * out rows of sequences with a length outside [1, L_max] (reported) are
+ * left as they were for the 8-bit formats, and undefined for native caches.
+ * workspace: HILS_WS_ATTN_DECODE for native caches; 8-bit formats need none
+ * (NULL, 0). */
+hils_status_t hils_attn_decode_cache(const hils_config_t* cfg, const void* q, const hils_paged_t* paged,
+                                     const hils_cache_t* cache, const int32_t* idx, const float* s_sel, void* out,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/* The cache as contiguous rows, e.g. for hils_attn_prefill over a prompt as
+ * decode will see it: k_out, v_out [B, Hkv, out_rows, d] (dtype) get at row p
+ * the values of position p < min(seq_lens[b], out_rows); other rows are left as
+ * they were.  Either output may be NULL.  A length of 0 reads nothing. */
+hils_status_t hils_cache_read(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
+                              void* k_out, void* v_out, int32_t out_rows, void* stream);
+
+/*
  * Device address of page-locked (pinned), mapped host memory, for keeping the
  * decode KV cache in host memory (the wmrh.cn article on HiLS: chunk-sparse
  * attention lets the unselected chunks of the cache stay off the GPU).  Passed
