@@ -741,6 +741,10 @@ static hils_status_t cache_args(const hils_config_t* cfg, const hils_paged_t* pa
     return fail(HILS_ERR_INVALID_ARG, "cache: unknown format %d", cache->format);
   HILS_TRY(make_shape(cfg, s, cache->format == HILS_KV_NATIVE ? native : kOpCache8));
   HILS_TRY(paged_view(*s, paged, dv));
+  // the 8-bit kernels address the pool by 128-byte lines in 32 bits
+  if (cache->format != HILS_KV_NATIVE &&
+      (long long)dv->num_pages * s->Hkv * (s->S * s->d / 128) > 0x7fffffffll)
+    return fail(HILS_ERR_UNSUPPORTED, "cache: a pool of %d pages has more than 2^31 lines of 128 bytes", dv->num_pages);
   return cache_view(*s, cache, cv);
 }
 

@@ -14,6 +14,10 @@ namespace hils {
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                            const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
+// Map of `rows` rows of 128 bytes, boxes of `box_rows` rows, 128-byte swizzle
+// (16-byte piece i of a row lands at piece i ^ (row & 7)).
+cudaError_t make_tmap_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
+
 // Multiprocessor count of the current device (queried once per device).
 int device_sm_count();
 

@@ -302,7 +302,7 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
  * tokens of its last chunk and the one before (its length reduced, other
  * tokens appended) as long as every token of those two chunks was appended
  * here.  8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
- * and dtype BF16 with d = 128, S = 64; native caches every shape of the
+ * and dtype BF16 with d = 128, S = 64, and pools of up to 256 GB; native caches every shape of the
  * summaries (hils_attn_decode_cache: those of hils_attn_decode_paged).
  * Pools, tails and scales are 16-byte aligned.
  */

@@ -7,13 +7,13 @@ rotated queries are defined by float32 operations in a given order: equal bits.
 For summaries and attention let mag = sum of weight * |value| (from the model):
   * an output element is a weighted sum of at most n held values.  The logits
     are float32 sums of d products: off by at most (d + 4) 2^-24 big, big =
-    max sum |q_e k_e| scale (the two scale factors round once each).  Shared
-    exponent: for float32 queries each element is held as two halves, off by
-    2^-24 of the row's largest; d such errors against |k| are covered by a
-    factor of two.  A weight is off by twice that (its numerator and its sum),
+    max sum |q_e k_e| scale (the two scale factors round once each).  Float32
+    queries are held as two halves, off by 2^-22 of themselves, which a factor
+    of two covers.  A weight is off by twice that (its numerator and its sum),
     and by 2^-20 for exp, log and the quotient;
   * float32 inputs: weights are held to 2^-22, sums of S products, then of units:
     (S + n / S + 16) 2^-24;
+  * no weight is resolved below 2^-40 of its chunk's largest (`low`);
   * bf16 inputs: weights round to half precision (2^-11), and the result to
     bf16 (2^-8 of itself).
 """
@@ -37,8 +37,8 @@ def weights_off(dtype, d, S, n, big):
     return off + (2.0 ** -22 if dtype is F32 else 2.0 ** -11)
 
 
-def out_off(dtype, got, want, mag, rel):
-    tol = mag * rel + (want.abs() * 2.0 ** -8 if dtype is BF else want.abs() * 2.0 ** -24)
+def out_off(dtype, got, want, mag, low, rel):
+    tol = mag * rel + low + (want.abs() * 2.0 ** -8 if dtype is BF else want.abs() * 2.0 ** -24)
     return ((got.double().cpu() - want).abs() - tol).max().item()
 
 
@@ -123,11 +123,11 @@ class Case:
     def check_attention(self, lens, q, idx, s_sel, out, accepted=None):
         for b, L in enumerate(lens):
             k, v = self.ref.values(0, b, L), self.ref.values(1, b, L)
-            want, mag, big = attend(q[b].double(), k, v, (idx if accepted is None else accepted)[b].tolist(),
+            want, mag, low, big = attend(q[b].double(), k, v, (idx if accepted is None else accepted)[b].tolist(),
                                     s_sel[b].double(), self.S, self.W, self.scale)
             n = self.K * self.S + self.W
             rel = weights_off(self.dtype, self.d, self.S, n, big)
-            assert out_off(self.dtype, out[b], want, mag, rel) <= 0, (b, L)
+            assert out_off(self.dtype, out[b], want, mag, low, rel) <= 0, (b, L)
 
 
 SHAPES = [(BF, 128, 64), (F32, 64, 32), (F32, 128, 64), (F32, 64, 64), (F32, 128, 32)]
@@ -432,10 +432,10 @@ def check_summaries(c, lens, first, q_lmk, k_sum, b_sum, blank_k, blank_b):
             continue
         k = c.ref.values(0, b, C * c.S)[:, first[b] * c.S:].reshape(c.Hkv, -1, c.S, c.d)
         ql = q_lmk(b, range(first[b], C))
-        want, ent, mag = summaries(k, ql, c.scale)
+        want, ent, mag, low = summaries(k, ql, c.scale)
         big = float((k.abs().amax(dim=2).repeat_interleave(c.Hq // c.Hkv, 0) * ql.abs()).sum(-1).max() * c.scale)
         rel = weights_off(c.dtype, c.d, c.S, c.S, big)
-        assert out_off(c.dtype, k_sum[b][:, first[b]:C], want, mag, rel) <= 0, b
+        assert out_off(c.dtype, k_sum[b][:, first[b]:C], want, mag, low, rel) <= 0, b
         # H(p) = -sum p log p: each p off by `eps` of itself moves it by at most eps (H + 1), and log and exp of
         # arguments up to `big` by 2^-22 of them
         eps = 2 * 2 * (c.d + 4) * 2.0 ** -24 * big + 2.0 ** -20 + (c.S + 16) * 2.0 ** -24
@@ -832,3 +832,30 @@ def test_two_streams_at_once_and_repeats_bit_for_bit():
     torch.cuda.synchronize()
     H.hils_sync_status()
     assert same(outs[0], want[0]) and same(outs[1], want[1])
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The test hook keeps the tile copies from being issued: the bounded waits run out, and the calls work again after."""
+    c = Case(2, 8, 2, 128, 64, 640, BF, I8, W=128, K=3)
+    lens = [640, 300]
+    c.fill(lens)
+    idx, s_sel = c.lists(lens)
+    q, q_lmk = c.rand(2, 8, 128), c.rand(2, 8, 10, 128).to(DEV)
+    args = (c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), torch.empty((2, 8, 128), dtype=BF, device=DEV))
+    sums = [torch.zeros((2, 8, 10, 128), dtype=BF, device=DEV), torch.zeros((2, 8, 10), device=DEV)]
+    H.hils_sync_status()
+    for run in (lambda: H.hils_attn_decode_cache(*args),
+                lambda: H.hils_build_summaries_cache(c.cfg, c.paged(lens), c.cache, q_lmk, *sums)):
+        try:
+            H.hils_set_wait_budget(2_000_000)  # about a millisecond
+            H.hils_set_fault_injection(1)
+            run()
+        finally:
+            H.hils_set_fault_injection(0)
+            H.hils_set_wait_budget(0)
+        with pytest.raises(H.HilsError) as e:
+            H.hils_sync_status()
+        assert e.value.status == H.HILS_ERR_TIMEOUT
+        run()
+        H.hils_sync_status()
+    c.check_attention(lens, q, idx, s_sel, args[-1])
