@@ -10,12 +10,12 @@
 // the configuration's type, and what the cache holds does not depend on how
 // tokens were split over calls.
 //
-// One launch.  The first CTAs take one (touched chunk, KV head, key or value)
-// each: rows of the call from the projection's output (keys rotated), earlier
-// rows of a chunk that completes from the tail, everything in registers
-// between load and store.  The others rotate the queries.
-// Both parts read each element once and write it once: memory-bound for
-// prompts, latency-bound (three dependent loads) for single tokens.
+// One launch with two kinds of CTAs in turn.  One takes a (touched chunk, KV
+// head): rows of the call from the projection's output (keys rotated), earlier
+// rows of a chunk that completes from the tail, everything in registers between
+// load and store.  The other rotates rows of the queries.  Both read each element
+// once and write it once.  Alone, the first is bound by its instructions and
+// waits (scale, then codes), the second by the memory, so they are mixed.
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -27,26 +27,47 @@ constexpr int kThreads = 256;
 constexpr float kTiny = 0x1p-110f;
 
 // ------------------------------------------------- eight elements at once ---
-HILS_DI void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// as they are in memory (a thread keeps several of them between load and store)
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+HILS_DI Raw8<T> load_raw(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
-HILS_DI void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+template <typename T>
+HILS_DI void store_raw(T* p, const Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+}
+HILS_DI void to_values(const Raw8<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.w[i].x), x[4 * i + 1] = __uint_as_float(r.w[i].y);
+    x[4 * i + 2] = __uint_as_float(r.w[i].z), x[4 * i + 3] = __uint_as_float(r.w[i].w);
+  }
+}
+HILS_DI void to_values(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_f32x2(r[i]);
+    const float2 f = bf16x2_to_f32x2(w[i]);
     x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
 }
-HILS_DI void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+HILS_DI void to_raw(const float (&x)[8], Raw8<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.w[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                        __float_as_uint(x[4 * i + 3]));
 }
-HILS_DI void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+HILS_DI void to_raw(const float (&x)[8], Raw8<__nv_bfloat16>& r) {
+  r.w[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
 }
 
 // ---------------------------------------------------------------- rotation ---
@@ -97,28 +118,57 @@ HILS_DI void rotate(const RopeView& rp, const float (&co)[8], const float (&si)[
   }
 }
 template <typename T>
-HILS_DI void round8(float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_f32(from_f32<T>(x[i]));
+HILS_DI void rotate_raw(const RopeView& rp, const float (&co)[8], const float (&si)[8], Raw8<T>& r0, Raw8<T>& r1) {
+  float x0[8], x1[8];
+  to_values(r0, x0);
+  to_values(r1, x1);
+  rotate(rp, co, si, x0, x1);
+  to_raw(x0, r0);
+  to_raw(x1, r1);
 }
 
 // ------------------------------------------------------------------- codes ---
+// Eight codes of x by.  int8: |x by| <= 127 (1 + 2^-22), so adding 1.5 2^23 rounds
+// it to an integer of at most 127, in the low byte, to nearest even.
 template <int FMT>
 HILS_DI uint2 encode8(const float (&x)[8], float by) {
-  uint32_t w[2] = {0u, 0u};
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __fmul_rn(x[2 * i], by), c = __fmul_rn(x[2 * i + 1], by);
-    uint32_t two;
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(x[4 * h + i], by);
     if (FMT == kI8) {
-      const int ia = max(-127, min(127, __float2int_rn(a))), ic = max(-127, min(127, __float2int_rn(c)));
-      two = (uint32_t)(ia & 0xff) | ((uint32_t)(ic & 0xff) << 8);
+      uint32_t z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+      w[h] = __byte_perm(__byte_perm(z[0], z[1], 0x0040), __byte_perm(z[2], z[3], 0x0040), 0x5410);
     } else {
-      two = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3),
+                     hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+      w[h] = lo | (hi << 16);
     }
-    w[i >> 1] |= two << (16 * (i & 1));
   }
   return make_uint2(w[0], w[1]);
+}
+// Largest magnitude of eight elements as the bits of a float32: magnitudes order
+// like their bits (NaN above infinity), also those of bf16 pairs in their halves.
+HILS_DI unsigned top_bits(unsigned top, const Raw8<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    top = max(max(top, max(r.w[i].x & 0x7fffffffu, r.w[i].y & 0x7fffffffu)),
+              max(r.w[i].z & 0x7fffffffu, r.w[i].w & 0x7fffffffu));
+  return top;
+}
+HILS_DI unsigned top_bits(unsigned top, const Raw8<__nv_bfloat16>& r) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+  unsigned low = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top = max(top, w[i] & 0x7fff0000u);
+    low = max(low, w[i] & 0x00007fffu);
+  }
+  return max(top, low << 16);
 }
 
 // ------------------------------------------------------------- the new rows ---
@@ -139,75 +189,118 @@ HILS_DI int angle_row(const NewRows& nr, const RopeView& rp, int r, int p, const
   return -1;
 }
 
+
+// Block numbers of the two kinds of CTAs, dealt in turn: after each one of the
+// fewer kind `per` - 1 of the other, and what is left of those at the end.
+struct CtaMix {
+  int fewer, per;
+  bool fewer_queries;
+  HILS_DI int part(int x, bool& queries) const {
+    const int round = x / per;
+    if (x >= fewer * per) {
+      queries = !fewer_queries;
+      return x - fewer;
+    }
+    queries = (x == round * per) == fewer_queries;
+    return x == round * per ? round : x - round - 1;
+  }
+};
+
 template <typename T, int FMT, int D, int S>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(Shape s, CacheView cv, DecView dv, NewRows nr,
-                                                                RopeView rp, int kv_ctas, int q_lanes, DevCtx ctx) {
+__global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
+    Shape s, CacheView cv, DecView dv, NewRows nr, RopeView rp, CtaMix mix, int q_lanes, DevCtx ctx) {
   constexpr int SLOTS = D / 16;  // two groups of eight elements each
-  constexpr int ITEMS = S * SLOTS, NI = (ITEMS + kThreads - 1) / kThreads;
+  constexpr int STEP = kThreads / SLOTS, NI = (S + STEP - 1) / STEP;  // rows of a pass, passes over a chunk
+  constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;  // heads that a thread of the queries' part has in flight
   __shared__ int sh_b;
   __shared__ int sh_seq[kThreads / 2];
-  __shared__ unsigned sh_top[kThreads / 32];
-  const int tid = threadIdx.x;
+  __shared__ unsigned sh_top[2][kThreads / 32];
+  const int tid = threadIdx.x, slot = tid % SLOTS;
+  int e0, e1;  // the thread's groups of every row
+  slot_groups(slot, rp.rot, e0, e1);
+  bool queries;
+  const int cta = mix.part(blockIdx.x, queries);
 
-  if ((int)blockIdx.x >= kv_ctas) {
-    // ---- queries: thread = (row, slot, one of q_lanes heads), heads in strides,
-    // so that a row's angles are loaded once for several heads
-    if (!nr.q) return;
+  if (queries) {
+    // ---- queries: thread = (row, slot, one of q_lanes heads and those that follow
+    // in steps of q_lanes), one load of the angles for all of them.  The first
+    // loads are asked for before the row's sequence is known.
     const int per_row = SLOTS * q_lanes, rows = kThreads / per_row;
-    const int t0 = ((int)blockIdx.x - kv_ctas) * rows;
+    const int t0 = cta * rows;
+    const int i = tid / per_row, t = t0 + i, h0 = (tid % per_row) / SLOTS;
+    const bool live = i < rows && t < nr.n_rows;
+    Raw8<T> r0[kHeads], r1[kHeads];
+    const T* q = (const T*)nr.q + (long long)t * nr.q_row;
+    auto ask = [&](int hb) {
+#pragma unroll
+      for (int x = 0; x < kHeads; ++x) {
+        const int h = hb + x * q_lanes;
+        if (live && h < s.Hq) {
+          r0[x] = load_raw(q + h * nr.q_head + e0);
+          r1[x] = load_raw(q + h * nr.q_head + e1);
+        }
+      }
+    };
+    ask(h0);
     if (tid < rows) sh_seq[tid] = -1;
     __syncthreads();
     for (int b = tid; b < s.B; b += kThreads) {
-      int r0, r1;
-      if (!seq_rows(nr, b, r0, r1)) continue;
-      for (int t = max(r0, t0); t < min(r1, t0 + rows); ++t) sh_seq[t - t0] = b;
+      int a, z;
+      if (!seq_rows(nr, b, a, z)) continue;
+      for (int y = max(a, t0); y < min(z, t0 + rows); ++y) sh_seq[y - t0] = b;
     }
     __syncthreads();
-    const int i = tid / per_row;
-    if (i >= rows || sh_seq[i] < 0) return;
-    const int b = sh_seq[i], t = t0 + i;
-    const int r0 = row_begin(nr, b), r1 = row_begin(nr, b + 1);
+    if (!live || sh_seq[i] < 0) return;
+    const int b = sh_seq[i], a = row_begin(nr, b), z = row_begin(nr, b + 1);
     const int L = dv_len(dv, s, b);
-    if (!len_fits(s, L, r1 - r0)) return;  // reported by the cache's part
-    const int slot = tid % SLOTS;
-    int e0, e1;
-    slot_groups(slot, rp.rot, e0, e1);
+    if (!len_fits(s, L, z - a)) return;  // reported by the cache's part
     int at = -1;
     float co[8], si[8];
     if (16 * slot < rp.rot) {
-      at = angle_row(nr, rp, t, L - (r1 - t), ctx);
+      at = angle_row(nr, rp, t, L - (z - t), ctx);
       if (at >= 0) load_angles(rp, at, e0, e1, co, si);
     }
-    const T* q = (const T*)nr.q + (long long)t * nr.q_row;
     T* o = (T*)nr.q_out + (long long)t * nr.q_out_row;
-    for (int h = (tid % per_row) / SLOTS; h < s.Hq; h += q_lanes) {
-      float x0[8], x1[8];
-      load8(q + h * nr.q_head + e0, x0);
-      load8(q + h * nr.q_head + e1, x1);
-      if (at >= 0) rotate(rp, co, si, x0, x1);
-      store8(o + h * nr.q_out_head + e0, x0);
-      store8(o + h * nr.q_out_head + e1, x1);
+    for (int hb = h0;;) {
+#pragma unroll
+      for (int x = 0; x < kHeads; ++x) {
+        const int h = hb + x * q_lanes;
+        if (h >= s.Hq) break;
+        if (at >= 0) rotate_raw(rp, co, si, r0[x], r1[x]);
+        store_raw(o + h * nr.q_out_head + e0, r0[x]);
+        store_raw(o + h * nr.q_out_head + e1, r1[x]);
+      }
+      hb += kHeads * q_lanes;
+      if (hb >= s.Hq) break;
+      ask(hb);
     }
     return;
   }
 
-  // ---- cache: (unit, KV head, key or value).  Sequence b owns the units from
+  // ---- cache: (unit, KV head), keys and values.  Sequence b owns the units from
   // row_start[b] / S + 2 b on: floor(n / S) + 2 of them at least, and n rows
   // touch no more chunks than that.
-  const int vals = blockIdx.x & 1, g = (int)(blockIdx.x >> 1) % s.Hkv, u = (int)(blockIdx.x >> 1) / s.Hkv;
-  if (tid == 0) sh_b = -1;
-  __syncthreads();
-  for (int b = tid; b < s.B; b += kThreads) {
-    int r0, r1;
-    if (!seq_rows(nr, b, r0, r1)) {
-      if (blockIdx.x == 0) raise_status(ctx, kStatusBadIndex);
-      continue;
-    }
-    if (u >= r0 / S + 2 * b && u < r1 / S + 2 * b + 2) sh_b = b;
+  const int g = cta % s.Hkv, u = cta / s.Hkv;
+  int b = -1;
+  if (!nr.row_start) {
+    b = u / 2;  // one row each: units 2 b and 2 b + 1 (S > 1 rows to a unit of rows)
+    if (b >= s.B || u >= (b + 1) / S + 2 * b + 2 || u < b / S + 2 * b) b = -1;
   }
-  __syncthreads();
-  const int b = sh_b;
-  if (b < 0) return;
+  if (b < 0) {
+    if (tid == 0) sh_b = -1;
+    __syncthreads();
+    for (int x = tid; x < s.B; x += kThreads) {
+      int r0, r1;
+      if (!seq_rows(nr, x, r0, r1)) {
+        if (cta == 0) raise_status(ctx, kStatusBadIndex);
+        continue;
+      }
+      if (u >= r0 / S + 2 * x && u < r1 / S + 2 * x + 2) sh_b = x;
+    }
+    __syncthreads();
+    b = sh_b;
+    if (b < 0) return;
+  }
   const int r0 = row_begin(nr, b), n = row_begin(nr, b + 1) - r0;
   if (n == 0) return;
   const int L = dv_len(dv, s, b);
@@ -219,117 +312,126 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(Shape s, CacheVi
   const int c = c0 + (u - r0 / S - 2 * b);
   if (c > last) return;
   const bool whole = (c + 1) * S <= L;
-  const bool rot = !vals && rp.rot > 0;
-  const T* src = (const T*)(vals ? nr.v : nr.k) + g * (vals ? nr.v_head : nr.k_head);
-  const long long src_row = vals ? nr.v_row : nr.k_row;
   long long off = -1;
   if (FMT == kNative || whole) {
     off = dv_chunk(dv, s, b, g, c);
     if (off < 0 && tid == 0) raise_status(ctx, kStatusBadIndex);  // a page outside the pool: never written
   }
-  T* tail = FMT == kNative ? nullptr : (T*)(vals ? cv.v_tail : cv.k_tail);
+  // Rows before `first` of chunk c0, if it completes, are read from its tail slot
+  // here while chunks last - 1 and last write their slots: if one of those is the
+  // same slot, this CTA writes it, after its reads.
+  const bool reads_tail = FMT != kNative && first > c0 * S && c0 < last + ((last + 1) * S <= L);
+  const bool later = c > c0 && reads_tail && ((c ^ c0) & 1) == 0;
+  if (FMT == kNative ? off < 0 : later && !whole) return;
+  const T* src[2] = {(const T*)nr.k + g * nr.k_head, (const T*)nr.v + g * nr.v_head};
+  const long long src_row[2] = {nr.k_row, nr.v_row};
+  T* tails[2] = {(T*)cv.k_tail, (T*)cv.v_tail};
+  void* pools[2] = {cv.k_pool, cv.v_pool};
+  float* scales[2] = {cv.k_scale, cv.v_scale};
 
-  // new row of chunk cc at j, its slot's two groups, rotated and rounded to T
-  auto load_new = [&](int cc, int j, int slot, int e0, int e1, float (&x0)[8], float (&x1)[8]) {
-    const int p = cc * S + j, r = r0 + p - first;
-    load8(src + r * src_row + e0, x0);
-    load8(src + r * src_row + e1, x1);
-    if (rot && 16 * slot < rp.rot) {
-      const int at = angle_row(nr, rp, r, p, ctx);
-      if (at >= 0) {
-        float co[8], si[8];
-        load_angles(rp, at, e0, e1, co, si);
-        rotate(rp, co, si, x0, x1);
-        round8<T>(x0);
-        round8<T>(x1);
-      }
+  // the thread's groups of the new row at position p, and the rotation of a key's
+  auto load_new = [&](int x, int p, Raw8<T>& y0, Raw8<T>& y1) {
+    const T* row = src[x] + (r0 + p - first) * src_row[x];
+    y0 = load_raw(row + e0);
+    y1 = load_raw(row + e1);
+  };
+  auto rotate_new = [&](int p, Raw8<T>& y0, Raw8<T>& y1) {
+    if (16 * slot >= rp.rot) return;
+    const int at = angle_row(nr, rp, r0 + p - first, p, ctx);
+    if (at < 0) return;
+    float co[8], si[8];
+    load_angles(rp, at, e0, e1, co, si);
+    rotate_raw(rp, co, si, y0, y1);
+  };
+  // of the chunk's row j: the new row, or for a chunk that completes the tail's
+  auto load_item = [&](int x, int j, Raw8<T>& y0, Raw8<T>& y1) {
+    const int p = c * S + j;
+    if (j >= S || p >= L) return;
+    if (p >= first) {
+      load_new(x, p, y0, y1);
+    } else if (FMT != kNative && whole) {
+      const T* t = tails[x] + tail_off(s, b, g, c) + j * D;
+      y0 = load_raw(t + e0);
+      y1 = load_raw(t + e1);
     }
   };
+  const int j0 = tid / SLOTS;
 
-  if constexpr (FMT == kNative) {
-    if (off < 0) return;
-    T* page = (T*)(vals ? cv.v_pool : cv.k_pool) + off;
+  // bf16: keys and values are asked for together, 32 KB of loads in flight for a CTA
+  constexpr bool kBoth = sizeof(T) == 2;
+  Raw8<T> x0[kBoth ? 2 : 1][NI], x1[kBoth ? 2 : 1][NI];
+  if (kBoth) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int item = tid + i * kThreads, j = item / SLOTS, slot = item % SLOTS;
-      if (item >= ITEMS || c * S + j < first || c * S + j >= L) continue;
-      int e0, e1;
-      slot_groups(slot, rp.rot, e0, e1);
-      float x0[8], x1[8];
-      load_new(c, j, slot, e0, e1, x0, x1);
-      store8(page + j * D + e0, x0);
-      store8(page + j * D + e1, x1);
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) load_item(x, j0 + i * STEP, x0[kBoth ? x : 0][i], x1[kBoth ? x : 0][i]);
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    Raw8<T>(&y0)[NI] = x0[kBoth ? x : 0];
+    Raw8<T>(&y1)[NI] = x1[kBoth ? x : 0];
+    if (!kBoth) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) load_item(x, j0 + i * STEP, y0[i], y1[i]);
     }
-  } else {
-    // Rows before `first` of chunk c0, if it completes, are read from its tail
-    // slot here while chunks last - 1 and last write their slots: if one of
-    // those is the same slot, this CTA writes it, after its reads.
-    const bool reads_tail = first > c0 * S && c0 < last + ((last + 1) * S <= L);
-    const bool later = c > c0 && reads_tail && ((c ^ c0) & 1) == 0;
-    if (later && !whole) return;
-    float x0[NI][8], x1[NI][8];
     unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int item = tid + i * kThreads, j = item / SLOTS, slot = item % SLOTS, p = c * S + j;
-      const bool is_new = item < ITEMS && p >= first && p < L;
-      if (!is_new && !(whole && item < ITEMS)) continue;
-      int e0, e1;
-      slot_groups(slot, rp.rot, e0, e1);
-      if (is_new) {
-        load_new(c, j, slot, e0, e1, x0[i], x1[i]);
-        if (c >= last - 1 && !later) {
-          T* t = tail + tail_off(s, b, g, c) + j * D;
-          store8(t + e0, x0[i]);
-          store8(t + e1, x1[i]);
+      const int j = j0 + i * STEP, p = c * S + j;
+      if (j < S && p >= first && p < L) {
+        if (x == 0) rotate_new(p, y0[i], y1[i]);
+        if (FMT == kNative) {
+          T* page = (T*)pools[x] + off;
+          store_raw(page + j * D + e0, y0[i]);
+          store_raw(page + j * D + e1, y1[i]);
+        } else if (c >= last - 1 && !later) {
+          T* t = tails[x] + tail_off(s, b, g, c) + j * D;
+          store_raw(t + e0, y0[i]);
+          store_raw(t + e1, y1[i]);
         }
-      } else {
-        const T* t = tail + tail_off(s, b, g, c) + j * D;
-        load8(t + e0, x0[i]);
-        load8(t + e1, x1[i]);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)  // magnitudes order like their bits; NaN above infinity
-        top = max(top, max(__float_as_uint(x0[i][k]) & 0x7fffffffu, __float_as_uint(x1[i][k]) & 0x7fffffffu));
+      if (FMT != kNative && whole && j < S) {
+        top = top_bits(top, y0[i]);
+        top = top_bits(top, y1[i]);
+      }
     }
-    if (!whole) return;
+    if (FMT == kNative || !whole) continue;
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) sh_top[tid >> 5] = top;
+    if ((tid & 31) == 0) sh_top[x][tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = max(top, sh_top[w]);
-    if (off >= 0) {
-      const float A = __uint_as_float(top), M = max_code(FMT);
-      const bool fine = top < 0x7f800000u, zero = fine && A < kTiny, held = fine && !zero;
-      const float by = held ? __fdiv_rn(M, A) : 0.f;
-      uint8_t* page = (uint8_t*)(vals ? cv.v_pool : cv.k_pool) + off;
+    for (int w = 0; w < kThreads / 32; ++w) top = max(top, sh_top[x][w]);
+    if (off < 0) continue;
+    const float A = __uint_as_float(top), M = max_code(FMT);
+    const bool fine = top < 0x7f800000u, zero = fine && A < kTiny, held = fine && !zero;
+    const float by = held ? __fdiv_rn(M, A) : 0.f;
+    uint8_t* page = (uint8_t*)pools[x] + off;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int item = tid + i * kThreads, j = item / SLOTS, slot = item % SLOTS;
-        if (item >= ITEMS) continue;
-        int e0, e1;
-        slot_groups(slot, rp.rot, e0, e1);
-        const uint2 z = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(page + j * D + e0) = held ? encode8<FMT>(x0[i], by) : z;
-        *reinterpret_cast<uint2*>(page + j * D + e1) = held ? encode8<FMT>(x1[i], by) : z;
-      }
-      if (tid == 0)
-        (vals ? cv.v_scale : cv.k_scale)[off / (S * D)] =
-            !fine ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(A, M);
+    for (int i = 0; i < NI; ++i) {
+      const int j = j0 + i * STEP;
+      if (j >= S) continue;
+      float z0[8], z1[8];
+      to_values(y0[i], z0);
+      to_values(y1[i], z1);
+      const uint2 none = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(page + j * D + e0) = held ? encode8<FMT>(z0, by) : none;
+      *reinterpret_cast<uint2*>(page + j * D + e1) = held ? encode8<FMT>(z1, by) : none;
     }
-    if (c == c0 && reads_tail) {
-      for (int cc = max(last - 1, c0 + 1); cc <= last; ++cc) {
-        if ((cc ^ c0) & 1) continue;
-        for (int item = tid; item < ITEMS; item += kThreads) {
-          const int j = item / SLOTS, slot = item % SLOTS;
-          if (cc * S + j >= L) continue;
-          int e0, e1;
-          slot_groups(slot, rp.rot, e0, e1);
-          float y0[8], y1[8];
-          load_new(cc, j, slot, e0, e1, y0, y1);
-          T* t = tail + tail_off(s, b, g, cc) + j * D;
-          store8(t + e0, y0);
-          store8(t + e1, y1);
+    if (tid == 0)
+      scales[x][off / (S * D)] = !fine ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(A, M);
+  }
+  if (FMT != kNative && whole && c == c0 && reads_tail) {  // every thread has read its tail rows (the barriers above)
+    for (int cc = max(last - 1, c0 + 1); cc <= last; ++cc) {
+      if ((cc ^ c0) & 1) continue;
+      for (int j = j0; j < S && cc * S + j < L; j += STEP) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          Raw8<T> y0, y1;
+          load_new(x, cc * S + j, y0, y1);
+          if (x == 0) rotate_new(cc * S + j, y0, y1);
+          T* t = tails[x] + tail_off(s, b, g, cc) + j * D;
+          store_raw(t + e0, y0);
+          store_raw(t + e1, y1);
         }
       }
     }
@@ -340,28 +442,54 @@ template <typename T, int FMT, int D, int S>
 cudaError_t go_append(const Shape& s, const CacheView& cv, const DecView& dv, const NewRows& nr, const RopeView& rp,
                       cudaStream_t st, const DevCtx& ctx) {
   constexpr int SLOTS = D / 16;
-  const long long kv = ((long long)nr.n_rows / S + 2ll * s.B) * s.Hkv * 2;
-  // lanes of a row: all heads for few rows (latency); a quarter of them for
-  // many, so that one load of the angles serves four heads
+  const long long kv = ((long long)nr.n_rows / S + 2ll * s.B) * s.Hkv;
+  // lanes of a row: all heads at once for few rows (latency); a quarter (float32:
+  // half) of them for many, so that one load of the angles serves several heads
+  constexpr int per = sizeof(T) == 2 ? 4 : 2;
   int lanes = s.Hq < kThreads / SLOTS ? s.Hq : kThreads / SLOTS;
-  if (nr.n_rows >= 2048 && lanes >= 4) lanes /= 4;
+  if (nr.n_rows >= 2048) lanes = (lanes + per - 1) / per;
   int rows = kThreads / (SLOTS * lanes);
   if (rows > kThreads / 2) rows = kThreads / 2;
   const long long qc = nr.q ? (nr.n_rows + rows - 1) / rows : 0;
   if (kv + qc > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const long long few = kv < qc ? kv : qc, many = kv < qc ? qc : kv;
+  CtaMix mix;
+  mix.fewer = (int)few;
+  mix.per = few ? (int)(many / few) + 1 : 1;
+  mix.fewer_queries = qc <= kv;
   cache_append_kernel<T, FMT, D, S>
-      <<<(unsigned)(kv + qc), kThreads, 0, st>>>(s, cv, dv, nr, rp, (int)kv, lanes, ctx);
+      <<<(unsigned)(kv + qc), kThreads, 0, st>>>(s, cv, dv, nr, rp, mix, lanes, ctx);
   return cudaGetLastError();
 }
 
 // ------------------------------------------------------------- reading back ---
 HILS_DI float decode1(int8_t c) { return (float)c; }
 HILS_DI float decode1(__nv_fp8_e4m3 c) { return (float)c; }
-HILS_DI float decode1(float c) { return c; }
-HILS_DI float decode1(__nv_bfloat16 c) { return to_f32(c); }
+
+// 32 bytes, a whole sector, at once
+HILS_DI void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+HILS_DI void store16(float* p, const float (&x)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
+    store32(p + 8 * h, w);
+  }
+}
+HILS_DI void store16(__nv_bfloat16* p, const float (&x)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  store32(p, w);
+}
 
 // One CTA per (chunk, KV head, sequence; keys or values): a tile is contiguous
-// in the pool and in the output.  Thread: groups of eight elements.
+// in the pool and in the output.
 template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView cv, DecView dv, T* __restrict__ k_out,
                                                               T* __restrict__ v_out, int out_rows, DevCtx ctx) {
@@ -378,37 +506,29 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView
   if (rows <= 0) return;
   out += (((long long)b * s.Hkv + g) * out_rows + (long long)c * s.S) * s.d;
   const int n = rows * s.d;
-  if (coded && (c + 1) * s.S > L) {  // the incomplete chunk
-    const T* t = (const T*)(vals ? cv.v_tail : cv.k_tail) + tail_off(s, b, g, c);
-    for (int e = threadIdx.x * 8; e < n; e += kThreads * 8) {
-      float x[8];
-      load8(t + e, x);
-      store8(out + e, x);
-    }
-    return;
-  }
-  const long long off = dv_chunk(dv, s, b, g, c);
+  const bool in_tail = coded && (c + 1) * s.S > L;  // the incomplete chunk
+  const long long off = in_tail ? 0 : dv_chunk(dv, s, b, g, c);
   if (off < 0) {
     if (threadIdx.x == 0) raise_status(ctx, kStatusBadIndex);
     return;
   }
+  if (!coded || in_tail) {
+    const T* t = in_tail ? (const T*)(vals ? cv.v_tail : cv.k_tail) + tail_off(s, b, g, c)
+                         : (const T*)(vals ? cv.v_pool : cv.k_pool) + off;
+#pragma unroll 4
+    for (int e = threadIdx.x * 8; e < n; e += kThreads * 8) store_raw(out + e, load_raw(t + e));
+    return;
+  }
   const C* page = (const C*)(vals ? cv.v_pool : cv.k_pool) + off;
-  if constexpr (coded) {
-    const float scale = __ldg((vals ? cv.v_scale : cv.k_scale) + off / (s.S * s.d));
-    for (int e = threadIdx.x * 8; e < n; e += kThreads * 8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(page + e);
-      float x[8];
-      const C* codes = reinterpret_cast<const C*>(&w);
+  const float scale = __ldg((vals ? cv.v_scale : cv.k_scale) + off / (s.S * s.d));
+#pragma unroll 2
+  for (int e = threadIdx.x * 16; e < n; e += kThreads * 16) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(page + e));
+    float x[16];
+    const C* codes = reinterpret_cast<const C*>(&w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = decode1(codes[i]) * scale;
-      store8(out + e, x);
-    }
-  } else {
-    for (int e = threadIdx.x * 8; e < n; e += kThreads * 8) {
-      float x[8];
-      load8(page + e, x);
-      store8(out + e, x);
-    }
+    for (int i = 0; i < 16; ++i) x[i] = decode1(codes[i]) * scale;
+    store16(out + e, x);
   }
 }
 

@@ -106,129 +106,217 @@ HILS_DI int dv_tile(const DecView& dv, const Shape& s, int b, int g, int c, cons
   return -1;
 }
 
+// which of code_mma.cuh's functions (measured there)
+template <typename T, typename C, int D, int S, int G>
+struct OpsOf {
+  using type = HalfOps<C, D, S, G, sizeof(T) == 4 ? 2 : 1>;
+};
+template <int D, int S>
+struct OpsOf<__nv_bfloat16, CodeI8, D, S, 1> {
+  using type = DigitOps<D, S, 1>;
+};
+template <int D, int S>
+struct OpsOf<__nv_bfloat16, CodeI8, D, S, 2> {
+  using type = DigitOps<D, S, 2>;
+};
+template <int D, int S>
+struct OpsOf<__nv_bfloat16, CodeI8, D, S, 4> {
+  using type = DigitOps<D, S, 4>;
+};
+
+// sc (logits) -> weights kOne e^{x - top}: `top` the column's largest logit, `l`
+// the weights' sum (float32); zl, if wanted, the sum of weight * (x - top)
+template <typename Ops, int N>
+HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = nullptr) {
+  top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    sc[i] *= mul;
+    top = fmaxf(top, sc[i]);
+  }
+  top = column_max(top);
+  const float m = top == -INFINITY ? 0.f : top;
+  l = 0.f;
+  float z = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x = sc[i] - m;
+    sc[i] = exp2_fast(fmaf(x, kLog2e, Ops::kLog2One));
+    l += sc[i];
+    if (zl) z += sc[i] * x;
+  }
+  l = column_sum(l);
+  if (zl) *zl = column_sum(z);
+}
+
+// Warps take the chunks of all sequences in turn, so that short and long
+// sequences share the work evenly.  A CTA serves sequences [kSeqs blockIdx.y, +
+// kSeqs): their numbers of chunks are summed up in shared memory, and unit u is
+// KV head u % Hkv of chunk u / Hkv of that order.  Two buffers for the tiles; the
+// landmark rows of the next unit are asked for before this one is computed.
+constexpr int kSeqs = 512;
+
 template <typename T, typename C, int D, int S, int G>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel(
     const __grid_constant__ CUtensorMap kmap, Shape s, CacheView cv, DecView dv, const T* __restrict__ q_lmk,
     LmkStrides ls, const int* __restrict__ from, T* __restrict__ k_sum, float* __restrict__ b_sum, DevCtx ctx) {
-  constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+  using Ops = typename OpsOf<T, C, D, S, G>::type;
+  constexpr int R = Ops::R, N8 = D / 8;
+  constexpr int PER = kSeqs / (kWarps * 32);  // sequences of a thread
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = align_1k(smem_raw);
   __shared__ uint64_t bars[kWarps][2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c4 = lane & 3;
-  const int g = blockIdx.y, b = blockIdx.z;
-  WarpBuffers<D, S>& buf = reinterpret_cast<WarpBuffers<D, S>*>(smem)[warp];
-  const int L = dv_len(dv, s, b), F = from ? __ldg(from + b) : 0;
-  if (L < 1 || L > s.N || F < 0) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) raise_status(ctx, kStatusBadIndex);
-    return;
-  }
-  const int step = gridDim.x * kWarps, end = L / S;
-  const int c_first = F / S + blockIdx.x * kWarps + warp;
-  if (c_first >= end) return;
+  __shared__ int ends[kSeqs], firsts[kSeqs], sums[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, c4 = lane & 3;
+  const int b0 = blockIdx.y * kSeqs, nb = min(kSeqs, s.B - b0);
+  WarpBuffers<D, S>& buf = reinterpret_cast<WarpBuffers<D, S>*>(align_1k(smem_raw))[warp];
   uint64_t* bar = bars[warp];
   if (lane == 0) {
+    prefetch_tmap(&kmap);
     mbar_init(&bar[0], 1);
     mbar_init(&bar[1], 1);
     fence_barrier_init();
     fence_proxy_async_shared();
   }
-  __syncwarp();
-  // lane l: tile and scale of the warp's unit l of the next 32
-  int my_tile = -1;
+  // chunks up to and with each sequence
+  int n[PER], own = 0;
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int b = tid * PER + x;
+    n[x] = 0;
+    if (b < nb) {
+      const int L = dv_len(dv, s, b0 + b), F = from ? __ldg(from + b0 + b) : 0;
+      const bool ok = L >= 1 && L <= s.N && F >= 0;
+      if (!ok && blockIdx.x == 0) raise_status(ctx, kStatusBadIndex);
+      firsts[b] = F / S;
+      n[x] = ok ? max(0, L / S - F / S) : 0;
+    }
+    own += n[x];
+  }
+  int upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += sums[w];
+    total += sums[w];
+  }
+  upto -= own;
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    upto += n[x];
+    if (tid * PER + x < nb) ends[tid * PER + x] = upto;
+  }
+  __syncthreads();
+  const long long units = (long long)total * s.Hkv, step = (long long)gridDim.x * kWarps;
+  long long u = (long long)blockIdx.x * kWarps + warp;
+  if (u >= units) return;
+  const TileOffsets<D> at(gq, c4);
+
+  // lane l: sequence, chunk, tile and scale of the warp's unit l of the next 32
+  int my_b = 0, my_c = 0, my_tile = -1;
   float my_scale = 0.f;
-  auto look_up = [&](int c0) {
-    const int c = c0 + lane * step;
-    my_tile = c < end ? dv_tile(dv, s, b, g, c, ctx, true) : -1;
+  auto look_up = [&](long long u0) {
+    const long long v = u0 + lane * step;
+    my_tile = -1;
+    if (v < units) {
+      const int t = (int)(v / s.Hkv);
+      int lo = 0, hi = nb - 1;  // the first sequence that ends behind t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > t) hi = mid;
+        else lo = mid + 1;
+      }
+      my_b = b0 + lo;
+      my_c = firsts[lo] + t - (lo ? ends[lo - 1] : 0);
+      my_tile = dv_tile(dv, s, my_b, (int)(v % s.Hkv), my_c, ctx, true);
+    }
     my_scale = my_tile >= 0 ? __ldg(cv.k_scale + my_tile) : 0.f;
   };
-  look_up(c_first);
-  int held = my_tile;  // tiles of units [base, base + 32)
-  float held_scale = my_scale;
-  int tile = __shfl_sync(0xffffffffu, held, 0);
-  if (lane == 0 && tile >= 0) fetch_tile<D, S>(buf.a, &kmap, tile, &bar[0], ctx);
-  bool flying[2] = {tile >= 0, false};
+  struct Unit {
+    int b, c, tile;
+    float ks;
+  };
+  auto unit_of = [&](int i) {
+    Unit x;
+    x.b = __shfl_sync(0xffffffffu, my_b, i & 31);
+    x.c = __shfl_sync(0xffffffffu, my_c, i & 31);
+    x.tile = __shfl_sync(0xffffffffu, my_tile, i & 31);
+    x.ks = __shfl_sync(0xffffffffu, my_scale, i & 31);
+    return x;
+  };
+  const int row = Ops::row_head(gq);
+  auto ask_query = [&](const Unit& x, long long v, RawRow<T, D>& raw) {
+    raw.load(row < G ? q_lmk + ls.of(x.b, (int)(v % s.Hkv) * G + row, x.c) : (const T*)nullptr, c4);
+  };
+  look_up(u);
+  Unit now = unit_of(0);
+  RawRow<T, D> raw;
+  if (now.tile >= 0) {
+    if (lane == 0) fetch_tile<D, S>(buf.a, &kmap, now.tile, &bar[0], ctx);
+    ask_query(now, u, raw);
+  }
+  bool flying[2] = {now.tile >= 0, false};
   uint32_t phase[2] = {0u, 0u};
   bool alive = true;
-  int i = 0;
-  for (int c = c_first; c < end; c += step, ++i) {
+  for (int i = 0; u < units; u += step, ++i) {
     const int st = i & 1;
-    const float ks = __shfl_sync(0xffffffffu, held_scale, i & 31);
-    // the next unit's tile into the other buffer
-    int next = -1;
-    if (c + step < end) {
-      if (((i + 1) & 31) == 0) {
-        look_up(c + step);
-        held = my_tile;
-        held_scale = my_scale;
-      }
-      next = __shfl_sync(0xffffffffu, held, (i + 1) & 31);
-      if (lane == 0 && next >= 0) fetch_tile<D, S>(st ? buf.a : buf.b, &kmap, next, &bar[st ^ 1], ctx);
-      flying[st ^ 1] = next >= 0;
+    Unit next;
+    next.tile = -1;
+    if (u + step < units) {
+      if (((i + 1) & 31) == 0) look_up(u + step);
+      next = unit_of(i + 1);
+      if (lane == 0 && next.tile >= 0) fetch_tile<D, S>(st ? buf.a : buf.b, &kmap, next.tile, &bar[st ^ 1], ctx);
+      flying[st ^ 1] = next.tile >= 0;
     }
-    if (tile >= 0) {
-      uint32_t qf[PARTS][D / 8];
-      const float up = load_qrow<T, C, D, PARTS>(gq < G ? q_lmk + ls.of(b, g * G + gq, c) : nullptr, c4, qf);
+    typename Ops::Query q;
+    if (now.tile >= 0) Ops::template make_query<T>(raw, gq, c4, q);
+    if (next.tile >= 0) ask_query(next, u + step, raw);
+    if (now.tile >= 0) {
       alive = mbar_wait(&bar[st], phase[st], ctx);
       if (!__all_sync(0xffffffffu, alive)) break;
       phase[st] ^= 1u;
       flying[st] = false;
       const uint8_t* t = st ? buf.b : buf.a;
-      float sc[S / 16][4], o[D / 16][4];
-      tile_scores<C, D, S, PARTS>(t, gq, c4, qf, sc);
-      float inv[2];
+      float sc[R][S / 8], o[R][N8], inv[R];
+      Ops::scores(t, at, q, sc);
+      const long long h0 = (long long)now.b * s.Hq + (u % s.Hkv) * G;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int h = 2 * c4 + r;
-        const float mul = s.scale * ks * __shfl_sync(0xffffffffu, up, 4 * h);
-        float m = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < S / 16; ++mt) {
-          sc[mt][r] *= mul;
-          sc[mt][2 + r] *= mul;
-          m = fmaxf(m, fmaxf(sc[mt][r], sc[mt][2 + r]));
-        }
-        m = column_max(m);
-        if (m == -INFINITY) m = 0.f;
-        float z = 0.f, zl = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < S / 16; ++mt)
-#pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            const float l = sc[mt][2 * hi + r] - m, e = weight_of(l);
-            sc[mt][2 * hi + r] = e;
-            z += e;
-            zl += e * l;
-          }
-        z = column_sum(z);
-        zl = column_sum(zl);
-        inv[r] = ks / z;
-        if (h < G && gq == 0) b_sum[((long long)b * s.Hq + g * G + h) * s.C + c] = logf(z * (1.f / kWeight1)) - zl / z;
+      for (int r = 0; r < R; ++r) {
+        const int h = Ops::head(r, c4);
+        float top, z, zl;
+        weigh<Ops>(sc[r], s.scale * now.ks * q.up[r], top, z, &zl);
+        inv[r] = __fdividef(now.ks, z);
+        if (h < G && gq == 0) b_sum[(h0 + h) * s.C + now.c] = logf(z * (1.f / Ops::kOne)) - __fdividef(zl, z);
       }
-      // weights e in half precision (2^-11 of each; float32: two parts), their sum in float32
-      tile_values<C, D, S, PARTS>(t, gq, c4, sc, o);
+      Ops::values(t, at, gq, sc, o);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int h = 2 * c4 + r;
+      for (int r = 0; r < R; ++r) {
+        const int h = Ops::head(r, c4);
         if (h >= G) continue;
-        T* dst = k_sum + (((long long)b * s.Hq + g * G + h) * s.C + c) * D + gq * (D / 8);
+        T* dst = k_sum + ((h0 + h) * s.C + now.c) * D + gq * N8;
+#pragma unroll
+        for (int x = 0; x < N8; ++x) o[r][x] *= inv[r];
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int v = 0; v < D / 64; ++v)
-            *reinterpret_cast<uint4*>(dst + 8 * v) =
-                make_uint4(pack_bf16x2(o[4 * v][r] * inv[r], o[4 * v][2 + r] * inv[r]),
-                           pack_bf16x2(o[4 * v + 1][r] * inv[r], o[4 * v + 1][2 + r] * inv[r]),
-                           pack_bf16x2(o[4 * v + 2][r] * inv[r], o[4 * v + 2][2 + r] * inv[r]),
-                           pack_bf16x2(o[4 * v + 3][r] * inv[r], o[4 * v + 3][2 + r] * inv[r]));
+          for (int x = 0; x < N8; x += 8)
+            *reinterpret_cast<uint4*>(dst + x) =
+                make_uint4(pack_bf16x2(o[r][x], o[r][x + 1]), pack_bf16x2(o[r][x + 2], o[r][x + 3]),
+                           pack_bf16x2(o[r][x + 4], o[r][x + 5]), pack_bf16x2(o[r][x + 6], o[r][x + 7]));
         } else {
 #pragma unroll
-          for (int v = 0; v < D / 32; ++v)
-            *reinterpret_cast<float4*>(dst + 4 * v) = make_float4(o[2 * v][r] * inv[r], o[2 * v][2 + r] * inv[r],
-                                                                  o[2 * v + 1][r] * inv[r], o[2 * v + 1][2 + r] * inv[r]);
+          for (int x = 0; x < N8; x += 4)
+            *reinterpret_cast<float4*>(dst + x) = make_float4(o[r][x], o[r][x + 1], o[r][x + 2], o[r][x + 3]);
         }
       }
     }
     __syncwarp();  // every lane has read the buffer that the next round refills
-    tile = next;
+    now = next;
   }
   if (!__all_sync(0xffffffffu, alive) && lane == 0)  // let the copies in flight land before the buffers go
     for (int st = 0; st < 2; ++st)
@@ -247,8 +335,10 @@ HILS_DI float peer_f32(const float* p, int rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
   return x;
 }
-// e^{a - M} for a <= M; 0 for a = -inf, also against M = -inf; NaN for a NaN
-HILS_DI float rel_weight(float a, float M) { return a == -INFINITY ? 0.f : exp_neg(a - M); }
+// A running maximum starts at -inf and is compared as no less than kLeast, so
+// that e^{a - M} is 0 for a = -inf (and NaN for a NaN) without a case of its own.
+constexpr float kLeast = -1e30f;
+HILS_DI float max_of(float a, float b) { return fmaxf(fmaxf(a, b), kLeast); }
 
 // eight elements as float32
 HILS_DI void row8(const float* p, float (&x)[8]) {
@@ -266,6 +356,7 @@ HILS_DI void row8(const __nv_bfloat16* p, float (&x)[8]) {
 }
 
 constexpr int kMaxUnits = 64 + 32;  // K list entries, W / S window chunks
+constexpr int kMaxWarps = 12;       // 16 KB of buffers each at d = 128, S = 64, up to 170 registers a thread
 
 // A cluster of CTAs serves one (sequence, KV head).  Units, dealt to the
 // cluster's warps in turn: 16-key slices of the incomplete chunk (in float32 on
@@ -274,19 +365,25 @@ constexpr int kMaxUnits = 64 + 32;  // K list entries, W / S window chunks
 // head, the CTA its warps, and the cluster its CTAs through distributed shared
 // memory: one launch, no workspace, a fixed order of adding.
 template <typename T, typename C, int D, int S, int G>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Shape s,
     const T* __restrict__ q, CacheView cv, DecView dv, const int32_t* __restrict__ idx,
     const float* __restrict__ s_sel, T* __restrict__ out, int ncta, DevCtx ctx) {
-  constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, MT = S / 16, OT = D / 16, N8 = D / 8;
+  using Ops = typename OpsOf<T, C, D, S, G>::type;
+  constexpr int R = Ops::R, N8 = D / 8;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = align_1k(smem_raw);
-  __shared__ uint64_t bars[kWarps][2];
+  __shared__ uint64_t bars[kMaxWarps][2];
   __shared__ int u_tile[kMaxUnits], u_slot[kMaxUnits], n_units;
-  __shared__ float u_ks[kMaxUnits], u_vs[kMaxUnits];
-  __shared__ float red_m[kWarps][G], red_d[kWarps][G], cta_m[G], cta_d[G];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c4 = lane & 3;
+  __shared__ float red_m[kMaxWarps][G], red_d[kMaxWarps][G], cta_m[G], cta_d[G];
+  unsigned char* smem = align_1k(smem_raw);
+  const int nwarp = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c4 = lane & 3;
   const int rank = blockIdx.x % ncta, g = (int)(blockIdx.x / ncta) % s.Hkv, b = (int)(blockIdx.x / ncta) / s.Hkv;
+  int e0 = -1, e1 = -1;  // the list (warp 0), asked for beside the length
+  if (warp == 0) {
+    const int32_t* ir = idx + ((long long)b * s.Hkv + g) * s.K;
+    if (lane < s.K) e0 = __ldg(ir + lane);
+    if (lane + 32 < s.K) e1 = __ldg(ir + lane + 32);
+  }
   const int L = dv_len(dv, s, b);
   if (L < 1 || L > s.N) {  // the whole cluster: reported, nothing written
     if (rank == 0 && threadIdx.x == 0) raise_status(ctx, kStatusBadIndex);
@@ -296,48 +393,39 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
   const int n_full = L / S - wc0, part = L % S, n_tail = (part + 15) / 16;
   uint64_t* bar = bars[warp];
   if (lane == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
     mbar_init(&bar[0], 1);
     mbar_init(&bar[1], 1);
     fence_barrier_init();
     fence_proxy_async_shared();
   }
-  const T* q0 = q + ((long long)b * s.Hq + g * G) * D;
-  uint32_t qf[PARTS][D / 8];
-  float qmul[2];
   if (warp == 0) {
     // the live units: window chunks, then accepted list entries (the list form, common.cuh)
-    const int32_t* ir = idx + ((long long)b * s.Hkv + g) * s.K;
-    int e0 = lane < s.K ? __ldg(ir + lane) : -1, e1 = lane + 32 < s.K ? __ldg(ir + lane + 32) : -1;
     bool bad;
     accept_list_warp(e0, e1, s.K, wc0, bad);
     if (bad && lane == 0 && rank == 0) raise_status(ctx, kStatusBadIndex);
     const int c[3] = {lane < n_full ? wc0 + lane : -1, e0, e1};
-    int n = 0;
+    int tile[3], n = 0;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) tile[x] = c[x] >= 0 ? dv_tile(dv, s, b, g, c[x], ctx, rank == 0) : -1;
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-      const int tile = c[x] >= 0 ? dv_tile(dv, s, b, g, c[x], ctx, rank == 0) : -1;
-      const unsigned live = __ballot_sync(0xffffffffu, tile >= 0);
-      if (tile >= 0) {
+      const unsigned live = __ballot_sync(0xffffffffu, tile[x] >= 0);
+      if (tile[x] >= 0) {
         const int at = n + __popc(live & ((1u << lane) - 1u));
-        u_tile[at] = tile;
+        u_tile[at] = tile[x];
         u_slot[at] = x == 0 ? -1 : lane + 32 * (x - 1);
-        u_ks[at] = __ldg(cv.k_scale + tile);
-        u_vs[at] = __ldg(cv.v_scale + tile);
       }
       n += __popc(live);
     }
     if (lane == 0) n_units = n;
   }
-  {
-    const float up = load_qrow<T, C, D, PARTS>(gq < G ? q0 + gq * D : nullptr, c4, qf);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) qmul[r] = s.scale * __shfl_sync(0xffffffffu, up, 4 * (2 * c4 + r));
-  }
   __syncthreads();
 
   WarpBuffers<D, S>& buf = reinterpret_cast<WarpBuffers<D, S>*>(smem)[warp];
-  const int step = ncta * kWarps, end = n_units + n_tail;
-  int i = rank * kWarps + warp;
+  const int step = ncta * nwarp, end = n_units + n_tail;
+  int i = rank * nwarp + warp;
   int first = i;  // the warp's first unit of codes
   while (first < n_tail) first += step;
   bool flying[2] = {false, false};
@@ -350,18 +438,54 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
     }
     flying[0] = flying[1] = true;
   }
+  const T* q0 = q + ((long long)b * s.Hq + g * G) * D;
+  const TileOffsets<D> at(gq, c4);
+  typename Ops::Query qr;
+  {
+    RawRow<T, D> raw;
+    raw.load(Ops::row_head(gq) < G ? q0 + Ops::row_head(gq) * D : (const T*)nullptr, c4);
+    Ops::template make_query<T>(raw, gq, c4, qr);
+  }
 
-  float acc[OT][4], M[2] = {-INFINITY, -INFINITY}, den[2] = {0.f, 0.f};
+  float acc[R][N8], M[R], den[R];
 #pragma unroll
-  for (int mt = 0; mt < OT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+  for (int r = 0; r < R; ++r) {
+    M[r] = -INFINITY;
+    den[r] = 0.f;
+#pragma unroll
+    for (int x = 0; x < N8; ++x) acc[r][x] = 0.f;
+  }
   // weights of a unit against the running maximum: fo for what is there, fu for the unit
   auto fold = [&](int r, float lam, float mass, float& fo, float& fu) {
-    const float Mn = fmaxf(M[r], lam);
-    fo = rel_weight(M[r], Mn);
-    fu = rel_weight(lam, Mn);
+    const float Mn = max_of(M[r], lam);
+    fo = exp_neg(M[r] - Mn);
+    fu = exp_neg(lam - Mn);
     den[r] = den[r] * fo + fu * mass;
     M[r] = Mn;
   };
+
+  // Of the warp's next 24 units: lane x holds the scales of unit x, lane (gq, c4)
+  // the scores of units gq, gq + 8, gq + 16 for its heads.
+  float my_ks, my_vs, my_s[R][3];
+  auto look_ahead = [&](int i0) {
+    my_ks = my_vs = 0.f;
+    if (i0 + lane * step < end) {
+      const int tile = u_tile[i0 + lane * step - n_tail];
+      my_ks = __ldg(cv.k_scale + tile);
+      my_vs = __ldg(cv.v_scale + tile);
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const int j = i0 + (gq + 8 * x) * step;
+      const int slot = j < end ? u_slot[j - n_tail] : -1;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        my_s[r][x] = slot >= 0 && Ops::head(r, c4) < G
+                         ? __ldg(s_sel + ((long long)b * s.Hq + g * G + Ops::head(r, c4)) * s.K + slot)
+                         : 0.f;
+    }
+  };
+  look_ahead(first);
 
   for (; i < n_tail; i += step) {
     // keys [16 i, 16 i + 16) of the incomplete chunk, in float32
@@ -369,113 +493,109 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
     const T* kt = (const T*)cv.k_tail + off;
     const T* vt = (const T*)cv.v_tail + off;
     const int nk = min(16, part - 16 * i);
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};  // key gq: columns 2 c4, 2 c4 + 1; key gq + 8
+    float sc[R][2];  // keys gq and gq + 8
+#pragma unroll
+    for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = 0.f;
 #pragma unroll 4
     for (int e = 0; e < D; e += 8) {
-      float k0[8], k1[8], qa[8], qb[8];
+      float k0[8], k1[8];
       row8(kt + min(gq, nk - 1) * D + e, k0);
       row8(kt + min(gq + 8, nk - 1) * D + e, k1);
-      row8(q0 + min(2 * c4, G - 1) * D + e, qa);
-      row8(q0 + min(2 * c4 + 1, G - 1) * D + e, qb);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        sc[0] = fmaf(k0[x], qa[x], sc[0]);
-        sc[1] = fmaf(k0[x], qb[x], sc[1]);
-        sc[2] = fmaf(k1[x], qa[x], sc[2]);
-        sc[3] = fmaf(k1[x], qb[x], sc[3]);
+      for (int r = 0; r < R; ++r) {
+        float qa[8];
+        row8(q0 + min(Ops::head(r, c4), G - 1) * D + e, qa);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          sc[r][0] = fmaf(k0[x], qa[x], sc[r][0]);
+          sc[r][1] = fmaf(k1[x], qa[x], sc[r][1]);
+        }
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sc[r] = gq < nk ? sc[r] * s.scale : -INFINITY;
-      sc[2 + r] = gq + 8 < nk ? sc[2 + r] * s.scale : -INFINITY;
-      const float top = column_max(fmaxf(sc[r], sc[2 + r])), m = top == -INFINITY ? 0.f : top;
-      sc[r] = exp_neg(sc[r] - m);
-      sc[2 + r] = exp_neg(sc[2 + r] - m);
+    for (int r = 0; r < R; ++r) {
+      sc[r][0] = gq < nk ? sc[r][0] * s.scale : -INFINITY;
+      sc[r][1] = gq + 8 < nk ? sc[r][1] * s.scale : -INFINITY;
+      const float top = column_max(fmaxf(sc[r][0], sc[r][1])), m = top == -INFINITY ? 0.f : top;
+      sc[r][0] = exp_neg(sc[r][0] - m);
+      sc[r][1] = exp_neg(sc[r][1] - m);
       float fo, fu;
-      fold(r, top, column_sum(sc[r] + sc[2 + r]), fo, fu);
-      sc[r] *= fu;
-      sc[2 + r] *= fu;
+      fold(r, top, column_sum(sc[r][0] + sc[r][1]), fo, fu);
+      sc[r][0] *= fu;
+      sc[r][1] *= fu;
 #pragma unroll
-      for (int mt = 0; mt < OT; ++mt) acc[mt][r] *= fo, acc[mt][2 + r] *= fo;
+      for (int x = 0; x < N8; ++x) acc[r][x] *= fo;
     }
 #pragma unroll 4
     for (int k = 0; k < nk; ++k) {
-      const float p0 = __shfl_sync(0xffffffffu, k < 8 ? sc[0] : sc[2], 4 * (k & 7) + c4);
-      const float p1 = __shfl_sync(0xffffffffu, k < 8 ? sc[1] : sc[3], 4 * (k & 7) + c4);
+      float p[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) p[r] = __shfl_sync(0xffffffffu, k < 8 ? sc[r][0] : sc[r][1], 4 * (k & 7) + c4);
 #pragma unroll
       for (int e = 0; e < N8; e += 8) {
         float v[8];
         row8(vt + k * D + gq * N8 + e, v);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int mt = (e + x) / 2, hi = 2 * (x & 1);
-          acc[mt][hi] = fmaf(p0, v[x], acc[mt][hi]);
-          acc[mt][hi + 1] = fmaf(p1, v[x], acc[mt][hi + 1]);
-        }
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) acc[r][e + x] = fmaf(p[r], v[x], acc[r][e + x]);
       }
     }
   }
 
-  for (i = first; i < end; i += step) {
-    const int u = i - n_tail, next = i + step < end ? u_tile[u + step] : -1, slot = u_slot[u];
-    const float ks = u_ks[u], vs = u_vs[u];
-    float shat[2] = {0.f, 0.f};
-    if (slot >= 0) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (2 * c4 + r < G) shat[r] = __ldg(s_sel + ((long long)b * s.Hq + g * G + 2 * c4 + r) * s.K + slot);
+  int n_done = 0;
+  for (i = first; i < end; i += step, ++n_done) {
+    if (n_done == 24) {
+      look_ahead(i);
+      n_done = 0;
     }
-    float sc[MT][4], o[OT][4];
+    const int u = i - n_tail, next = i + step < end ? u_tile[u + step] : -1;
+    const bool chosen = u_slot[u] >= 0;
+    const float ks = __shfl_sync(0xffffffffu, my_ks, n_done), vs = __shfl_sync(0xffffffffu, my_vs, n_done);
+    float sc[R][S / 8], o[R][N8], fo[R], fu[R];
     alive = mbar_wait(&bar[0], phase[0], ctx);
     if (!__all_sync(0xffffffffu, alive)) break;
     flying[0] = false;
     phase[0] ^= 1u;
-    tile_scores<C, D, S, PARTS>(buf.a, gq, c4, qf, sc);
+    Ops::scores(buf.a, at, qr, sc);
     __syncwarp();  // every lane has read the keys: their buffer takes the next unit's
     if (next >= 0) {
       if (lane == 0) fetch_tile<D, S>(buf.a, &kmap, next, &bar[0], ctx);
       flying[0] = true;
     }
-    float fo[2], fu[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float mul = qmul[r] * ks;
-      float top = -INFINITY;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        sc[mt][r] *= mul;
-        sc[mt][2 + r] *= mul;
-        top = fmaxf(top, fmaxf(sc[mt][r], sc[mt][2 + r]));
-      }
-      top = column_max(top);
-      const float m = top == -INFINITY ? 0.f : top;
-      float l = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        sc[mt][r] = weight_of(sc[mt][r] - m);
-        sc[mt][2 + r] = weight_of(sc[mt][2 + r] - m);
-        l += sc[mt][r] + sc[mt][2 + r];
-      }
-      l = column_sum(l);  // of weights times 2^15
+    for (int r = 0; r < R; ++r) {
+      float top, l;
+      weigh<Ops>(sc[r], s.scale * ks * qr.up[r], top, l);
       // a chosen chunk weighs e^{s^} whatever its l; a window chunk e^{top} l
-      fold(r, slot >= 0 ? shat[r] : top, slot >= 0 ? 1.f : l * (1.f / kWeight1), fo[r], fu[r]);
-      fu[r] *= slot >= 0 ? vs / l : vs * (1.f / kWeight1);
+      const float mine = n_done < 8 ? my_s[r][0] : n_done < 16 ? my_s[r][1] : my_s[r][2];
+      const float shat = __shfl_sync(0xffffffffu, mine, 4 * (n_done & 7) + c4);
+      fold(r, chosen ? shat : top, chosen ? 1.f : l * (1.f / Ops::kOne), fo[r], fu[r]);
+      fu[r] *= chosen ? __fdividef(vs, l) : vs * (1.f / Ops::kOne);
     }
     alive = mbar_wait(&bar[1], phase[1], ctx);
     if (!__all_sync(0xffffffffu, alive)) break;
     flying[1] = false;
     phase[1] ^= 1u;
-    tile_values<C, D, S, PARTS>(buf.b, gq, c4, sc, o);
+    Ops::values(buf.b, at, gq, sc, o);
     __syncwarp();
     if (next >= 0) {
       if (lane == 0) fetch_tile<D, S>(buf.b, &vmap, next, &bar[1], ctx);
       flying[1] = true;
     }
+    bool same = true;  // no column's maximum moved
 #pragma unroll
-    for (int mt = 0; mt < OT; ++mt)
+    for (int r = 0; r < R; ++r) same = same && fo[r] == 1.f;
+    if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[mt][x] = acc[mt][x] * fo[x & 1] + o[mt][x] * fu[x & 1];
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int x = 0; x < N8; ++x) acc[r][x] *= fo[r];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int x = 0; x < N8; ++x) acc[r][x] = fmaf(o[r][x], fu[r], acc[r][x]);
   }
   if (!__all_sync(0xffffffffu, alive) && lane == 0 && ctx.inject != 1) {
     // a wait ran out: let the copies in flight land before the buffers change hands
@@ -485,14 +605,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
   __syncthreads();  // every warp's copies have landed and been read: the buffers now hold the records
 
   float* rec = reinterpret_cast<float*>(smem);
-  float* cta = rec + kWarps * G * D;
+  float* cta = rec + nwarp * G * D;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int h = 2 * c4 + r;
+  for (int r = 0; r < R; ++r) {
+    const int h = Ops::head(r, c4);
     if (h >= G) continue;
 #pragma unroll
-    for (int mt = 0; mt < OT; ++mt)
-      *reinterpret_cast<float2*>(rec + (warp * G + h) * D + gq * N8 + 2 * mt) = make_float2(acc[mt][r], acc[mt][2 + r]);
+    for (int x = 0; x < N8; x += 4)
+      *reinterpret_cast<float4*>(rec + (warp * G + h) * D + gq * N8 + x) =
+          make_float4(acc[r][x], acc[r][x + 1], acc[r][x + 2], acc[r][x + 3]);
     if (gq == 0) {
       red_m[warp][h] = M[r];
       red_d[warp][h] = den[r];
@@ -500,15 +621,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
   }
   __syncthreads();
   T* o0 = out + ((long long)b * s.Hq + g * G) * D;
-  for (int x = threadIdx.x; x < G * D; x += kWarps * 32) {
+  for (int x = threadIdx.x; x < G * D; x += blockDim.x) {
     const int h = x / D;
-    float Mx = red_m[0][h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) Mx = fmaxf(Mx, red_m[w][h]);
+    float Mx = kLeast;
+    for (int w = 0; w < nwarp; ++w) Mx = fmaxf(Mx, red_m[w][h]);
     float num = 0.f, dd = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = rel_weight(red_m[w][h], Mx);
+    for (int w = 0; w < nwarp; ++w) {
+      const float f = exp_neg(red_m[w][h] - Mx);
       num += f * rec[w * G * D + x];
       dd += f * red_d[w][h];
     }
@@ -524,13 +643,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_codes_kernel(
   }
   if (ncta == 1) return;
   cluster_sync();
-  for (int x = rank * kWarps * 32 + threadIdx.x; x < G * D; x += ncta * kWarps * 32) {
+  for (int x = rank * blockDim.x + threadIdx.x; x < G * D; x += ncta * blockDim.x) {
     const int h = x / D;
-    float Mx = -INFINITY;
+    float Mx = kLeast;
     for (int w = 0; w < ncta; ++w) Mx = fmaxf(Mx, peer_f32(&cta_m[h], w));
     float num = 0.f, dd = 0.f;
     for (int w = 0; w < ncta; ++w) {
-      const float f = rel_weight(peer_f32(&cta_m[h], w), Mx);
+      const float f = exp_neg(peer_f32(&cta_m[h], w) - Mx);
       num += f * peer_f32(cta + x, w);
       dd += f * peer_f32(&cta_d[h], w);
     }
@@ -550,10 +669,12 @@ cudaError_t go_summ(const Shape& s, const CacheView& cv, const DecView& dv, cons
   CUtensorMap km;
   e = make_tmap_rows128(&km, cv.k_pool, (uint64_t)dv.num_pages * s.Hkv * (S * D / 128), S * D / 128);
   if (e != cudaSuccess) return e;
-  const int most = (s.C + kWarps - 1) / kWarps;
-  const int want = (device_sm_count() * kCtasPerSm * 2 + s.B * s.Hkv - 1) / (s.B * s.Hkv);
-  kern<<<dim3(want < most ? want : most, s.Hkv, s.B), kWarps * 32, smem, st>>>(km, s, cv, dv, (const T*)q_lmk, ls, from,
-                                                                                (T*)k_sum, b_sum, ctx);
+  // one wave of CTAs, fewer if there are not as many chunks
+  const int blocks = (s.B + kSeqs - 1) / kSeqs;
+  const long long most = ((long long)(s.B < kSeqs ? s.B : kSeqs) * s.C * s.Hkv + kWarps - 1) / kWarps;
+  const long long wave = (device_sm_count() * kCtasPerSm + blocks - 1) / blocks;
+  kern<<<dim3((unsigned)(wave < most ? wave : most), blocks), kWarps * 32, smem, st>>>(
+      km, s, cv, dv, (const T*)q_lmk, ls, from, (T*)k_sum, b_sum, ctx);
   return cudaGetLastError();
 }
 
@@ -574,33 +695,40 @@ cudaError_t go_native(const Shape& s, const CacheView& cv, const DecView& dv, co
 template <typename T, typename C, int D, int S, int G>
 cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const DecView& dv, const int32_t* idx,
                     const float* s_sel, void* out, cudaStream_t st, const DevCtx& ctx) {
-  const size_t smem = buffer_bytes<D, S>();
-  static_assert(sizeof(float) * (kWarps + 1) * G * D <= sizeof(WarpBuffers<D, S>) * kWarps, "records fit the buffers");
+  static_assert(2 * sizeof(float) * G * D <= sizeof(WarpBuffers<D, S>), "a warp's record and the CTA's fit the buffers");
   auto kern = attn_codes_kernel<T, C, D, S, G>;
-  cudaError_t e = ensure_dynamic_smem((const void*)kern, (int)smem);
+  cudaError_t e = ensure_dynamic_smem((const void*)kern, (int)(sizeof(WarpBuffers<D, S>) * kMaxWarps + 1024));
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)dv.num_pages * s.Hkv * (S * D / 128);
   e = make_tmap_rows128(&km, cv.k_pool, rows, S * D / 128);
   if (e == cudaSuccess) e = make_tmap_rows128(&vm, cv.v_pool, rows, S * D / 128);
   if (e != cudaSuccess) return e;
-  // CTAs of a cluster: as many as fit the device at once, and no more than there are units for
-  const int groups = s.B * s.Hkv, units = s.K + s.nw + 3;
-  int ncta = device_sm_count() * kCtasPerSm / groups;
-  ncta = ncta > 8 ? 8 : ncta;
-  ncta = ncta > (units + kWarps - 1) / kWarps ? (units + kWarps - 1) / kWarps : ncta;
-  ncta = ncta < 1 ? 1 : ncta;
+  // Warps for each (sequence, KV head): as many as put all of them on the device at
+  // once (twelve warps a multiprocessor), so that the memory is busy until they end
+  // together; 512 of them with three warps each 57.5 us, with four (two waves) 66.5.
+  // Below three a warp's own chain of units is the longer way: 768 with two 102 us,
+  // with four 95.  Few of them spread over clusters of CTAs, one multiprocessor
+  // each, down to one unit a warp.
+  const int sms = device_sm_count(), groups = s.B * s.Hkv, units = s.K + s.nw + 3;
+  int ncta = sms / groups;
+  ncta = ncta < 1 ? 1 : ncta > 8 ? 8 : ncta;
+  int share = sms * kMaxWarps / groups;
+  share = share < 3 ? 4 : share;
+  share = share < units ? share : units;
+  int nwarp = (share + ncta - 1) / ncta;
+  nwarp = nwarp > kMaxWarps ? kMaxWarps : nwarp;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)groups * ncta);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(nwarp * 32);
+  cfg.dynamicSmemBytes = sizeof(WarpBuffers<D, S>) * nwarp + 1024;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = ncta;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ncta > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, km, vm, s, (const T*)q, cv, dv, idx, s_sel, (T*)out, ncta, ctx);
 }
 

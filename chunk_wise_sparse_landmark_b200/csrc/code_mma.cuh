@@ -1,26 +1,40 @@
 // Warp-level building blocks for one tile of 8-bit codes (S keys x D dims, one
-// byte an element) in shared memory, with up to 8 query columns:
+// byte an element) in shared memory, against the query heads of a group:
 //
-//   S^T (S keys x 8 cols)  = X_tile (keys x D) . Q^T (D x cols)
-//   O^T (D x 8 cols)       = Y_tile^T (D x keys) . P^T (keys x cols)
+//   scores: S^T (S keys x columns) = X_tile (keys x D) . Q^T (D x columns)
+//   values: O^T (D x columns)      = Y_tile^T (D x keys) . P^T (keys x columns)
 //
-// half-precision mma.sync m16n8k16 with float32 accumulation.  Every code of
-// either format is exact in half precision (int8: integers up to 128; e4m3: 4
-// bits of significand, 2^-9 .. 448), so the only roundings are those of Q and P.
-// A query row is scaled by the power of two that brings its largest element
-// into [1, 2): bf16's 8 bits fit half precision's 11, and what falls below its
-// smallest step is off by 2^-25 of the row's largest element.  PARTS = 2 holds
-// float32 queries and weights as a sum of two halves (high and rest): off by
-// 2^-25 of the largest element as well.
+// Two sets of the same functions, both exact in the codes:
+//
+// * HalfOps: m16n8k16 in half precision, which holds every code of either format
+//   exactly (int8: integers up to 128; e4m3: four significant bits, 2^-9 .. 448),
+//   eight heads in the eight columns.  A query row is scaled by a power of two so
+//   that its largest element is in [2^14, 2^15): bf16's 8 bits fit half
+//   precision's 11, down to elements 2^-28 of the largest.  Weights e^{x - max}
+//   are computed times 2^15 for the same reason: within 2^-11 of themselves, or
+//   2^-40 of the largest.  PARTS = 2 (float32 configurations) holds queries and
+//   weights as a sum of two halves (the nearest one and the rest): within 2^-22.
+// * DigitOps (int8 codes, bf16, up to four heads): 8-bit m16n8k32 with int32 sums
+//   on the codes as they are.  A query or weight is a fixed-point number in 8-bit
+//   digits, each a column of its own: three for a query (within 2^-24 of its
+//   row's largest element: scores and entropies keep float32's accuracy), two
+//   for a weight (within 2^-16 of the largest), which only enters a result that
+//   rounds to bf16 (2^-8).
+// The sum of the weights is always taken in float32 from the unrounded ones.
+//
+// Which: widening costs an int8 code five instructions for four codes on the
+// pipe that limits, an e4m3 code two or three.  Decode attention over 64
+// sequences of 16K, K = 32, W = 512, us, DigitOps : HalfOps: int8, G = 1, 4, 8:
+// 63.8 : 68.5, 65.4 : 70.7, 92.4 : 67.7 (eight heads need two blocks of columns);
+// with e4m3 digits 70.6 : 66.0, 72.5 : 71.0, 96.1 : 73.0 (not kept).
 //
 // The tile is stored in lines of 128 bytes whose 16-byte pieces are swizzled as
 // TMA does (piece i of line r at i ^ (r & 7)); with gq = lane / 4, c4 = lane % 4:
-// * S^T: the contraction index is permuted, alike for X and Q: thread c4 holds
-//   the D / 4 dims from c4 D / 4 on, whole words of four codes, one word for
-//   each k-step.  The eight lanes that share one of a load's phases touch all
-//   eight pieces of a line once (no bank conflicts).
-// * O^T: row gq of m-tile mt is dim gq D / 8 + 2 mt, row gq + 8 the next one,
-//   so a thread's codes of a key are D / 8 contiguous bytes.
+// * scores: the contraction index is permuted, alike for X and Q: thread c4 holds
+//   the D / 4 dims from c4 D / 4 on, in words of four codes.  The eight lanes of
+//   one of a load's phases touch all eight pieces of a line once.  Result
+//   sc[r][2 mt + hi]: key 16 mt + gq + 8 hi, head head(r, c4).
+// * values: a thread holds dims gq D / 8 + x, x < D / 8: result o[r][x].
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,6 +55,26 @@ HILS_DI void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// D(16x8, s32) += A(16x32, s8, row) * B(32x8, s8, col)
+HILS_DI void mma_8bit(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same without a D to add to
+HILS_DI void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+HILS_DI void mma_8bit_first(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+}
 HILS_DI uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -50,13 +84,37 @@ HILS_DI uint32_t rest_f16x2(float lo, float hi, uint32_t w) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
   return pack_f16x2(lo - f.x, hi - f.y);
 }
+// 2^x (0 for -inf and wherever 2^x is below the normal range)
+HILS_DI float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+HILS_DI float exp_neg(float x) { return exp2_fast(x * kLog2e); }
+
+// byte offset of linear byte `o` of a tile
+HILS_DI int swz(int o) { return o ^ (((o >> 7) & 7) << 4); }
+// Offsets of a thread's parts in a tile; the pattern repeats every 16 keys.
+template <int D>
+struct TileOffsets {
+  static constexpr int V = D / 64;  // 16-byte pieces of a thread's dims of a key (scores)
+  int k[V][2];                      // piece v of key gq + 8 hi
+  int v[4];                         // keys 2 c4, + 1, + 8, + 9 (values)
+  HILS_DI TileOffsets(int gq, int c4) {
+#pragma unroll
+    for (int x = 0; x < V; ++x)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) k[x][hi] = swz((gq + 8 * hi) * D + c4 * (D / 4) + 16 * x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = swz((2 * c4 + (e & 1) + 8 * (e >> 1)) * D + gq * (D / 8));
+  }
+};
 
 // ------------------------------------------------------------------- codes ---
 // Two halves from two codes.  int8: a byte u = code + 128 below 0x64 is the half
 // 1024 + u, so subtracting 1152 leaves the code; even and odd bytes of a word
 // are taken apart by one mask.  e4m3: the conversion instruction, by half-words.
 struct CodeI8 {
-  static constexpr int kFormat = 1;
   // bytes {0, 2} and {1, 3} of w
   static HILS_DI void halves(uint32_t w, uint32_t& x, uint32_t& y) {
     x = sub((w & 0x00ff00ffu) ^ 0x64806480u);
@@ -67,6 +125,34 @@ struct CodeI8 {
   static HILS_DI uint32_t pair01(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
   static HILS_DI uint32_t pair23(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
+  // Digits of x0, x1 in [-kOne, kOne], as bytes lo, hi of x0, then of x1.  Adding
+  // 1.5 2^23 + 128 rounds x to an integer in the low bits, where y = x + 128 has
+  // hi = y >> 8 and lo = (y & 255) - 128.
+  static constexpr float kOne = 32512.f;  // 256 * 127
+  static HILS_DI uint32_t digits2(float x0, float x1) {
+    const float m = 12582912.f + 128.f;
+    return __byte_perm(__float_as_uint(x0 + m), __float_as_uint(x1 + m), 0x5410) ^ 0x00800080u;
+  }
+  static HILS_DI float join(int hi, int lo) { return (float)(256 * hi + lo); }
+  // Queries: integers up to kQuery in three digits, lo, mid, hi in bytes 0 .. 2.
+  static constexpr float kQuery = 127.f * 65536.f;
+  static HILS_DI void query4(const float (&x)[4], int odd, uint32_t (&w)[2]) {
+    uint32_t z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = (uint32_t)(__float2int_rn(x[i]) + 0x8080) ^ 0x8080u;
+    const uint32_t s0 = odd ? 0x51u : 0x62u;  // mid : hi
+    w[0] = __byte_perm(__byte_perm(z[0], z[1], s0), __byte_perm(z[2], z[3], s0), 0x5410);
+    w[1] = odd ? 0u : __byte_perm(__byte_perm(z[0], z[1], 0x40), __byte_perm(z[2], z[3], 0x40), 0x5410);
+  }
+  static HILS_DI float score(int hi, int mid, int lo) { return fmaf((float)(256 * hi + mid), 256.f, (float)lo); }
+  // the factor that brings a row's largest magnitude to kQuery, and its inverse
+  static HILS_DI void row_factor(float top, float& down, float& up) {
+    top = fmaxf(top, 0x1p-100f);  // smaller ones keep a finite factor
+    down = kQuery / top;
+    up = top * (1.f / kQuery);
+  }
+  static constexpr float kLog2One = 14.988684686772166f;
+
  private:
   static HILS_DI uint32_t sub(uint32_t h) {
     const uint32_t k = 0x64806480u;  // 1152
@@ -75,7 +161,6 @@ struct CodeI8 {
   }
 };
 struct CodeE4M3 {
-  static constexpr int kFormat = 2;
   // bytes {0, 1} and {2, 3} of w
   static HILS_DI void halves(uint32_t w, uint32_t& x, uint32_t& y) {
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
@@ -87,131 +172,42 @@ struct CodeE4M3 {
   static HILS_DI uint32_t pair23(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7362); }
 };
 
-// byte offset of linear byte `o` of a tile
-HILS_DI int swz(int o) { return o ^ (((o >> 7) & 7) << 4); }
-
-// ------------------------------------------------------------------ queries ---
-// Q^T B-fragments of column gq from that column's row (nullptr: zero column),
-// and the power of two that the row was divided by.
-template <typename T, typename C, int D, int PARTS>
-HILS_DI float load_qrow(const T* row, int c4, uint32_t (&qf)[PARTS][D / 8]) {
-  constexpr int N = D / 4;  // this thread's dims
-  float x[N];
+// A thread's part of a query row as it is in memory: the D / 4 elements from
+// c4 D / 4 on (zeros without a row).
+template <typename T, int D>
+struct RawRow {
+  static constexpr int N = D / 4, PER = 16 / sizeof(T);
+  uint4 w[N / PER];
+  HILS_DI void load(const T* row, int c4) {
+#pragma unroll
+    for (int v = 0; v < N / PER; ++v)
+      w[v] = row ? __ldg(reinterpret_cast<const uint4*>(row + c4 * N) + v) : make_uint4(0u, 0u, 0u, 0u);
+  }
+};
+// its elements as float32, and the bits of the whole row's largest magnitude
+template <typename T, int D>
+HILS_DI unsigned row_values(const RawRow<T, D>& raw, float (&x)[D / 4]) {
+  constexpr int N = D / 4, PER = 16 / sizeof(T);
   unsigned top = 0;
-  if (row) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + c4 * N);
-    constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-    for (int v = 0; v < N / PER; ++v) {
-      const uint4 w = __ldg(p + v);
-      const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+  for (int v = 0; v < N / PER; ++v) {
+    const uint32_t r[4] = {raw.w[v].x, raw.w[v].y, raw.w[v].z, raw.w[v].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (sizeof(T) == 2) {
-          const float2 f = bf16x2_to_f32x2(r[i]);
-          x[v * PER + 2 * i] = f.x;
-          x[v * PER + 2 * i + 1] = f.y;
-        } else {
-          x[v * PER + i] = __uint_as_float(r[i]);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.f;
-  }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // the largest element's exponent (that of 1 for a row that is zero or not finite), less 14
-  unsigned ex = top >> 23;
-  ex = top == 0 || ex == 255 ? 127 : max(ex, 15u);
-  const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex - 14u) << 23);
-#pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const float a = x[4 * ks] * down, b = x[4 * ks + C::kX1] * down, c = x[4 * ks + C::kY0] * down,
-                d = x[4 * ks + 3] * down;
-    qf[0][2 * ks] = pack_f16x2(a, b);
-    qf[0][2 * ks + 1] = pack_f16x2(c, d);
-    if (PARTS == 2) {
-      qf[PARTS - 1][2 * ks] = rest_f16x2(a, b, qf[0][2 * ks]);
-      qf[PARTS - 1][2 * ks + 1] = rest_f16x2(c, d, qf[0][2 * ks + 1]);
-    }
-  }
-  return up;
-}
-
-// ------------------------------------------------------------------ products ---
-// sc = S^T of the tile: sc[mt][0, 1] key 16 mt + gq, columns 2 c4 and 2 c4 + 1;
-// sc[mt][2, 3] key 16 mt + gq + 8
-template <typename C, int D, int S, int PARTS>
-HILS_DI void tile_scores(const uint8_t* t, int gq, int c4, const uint32_t (&qf)[PARTS][D / 8], float (&sc)[S / 16][4]) {
-  constexpr int V = D / 64;  // 16-byte pieces of a thread's row part
-#pragma unroll
-  for (int mt = 0; mt < S / 16; ++mt) {
-    sc[mt][0] = sc[mt][1] = sc[mt][2] = sc[mt][3] = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int o = (16 * mt + gq) * D + c4 * (D / 4) + 16 * v;
-      const uint4 a = *reinterpret_cast<const uint4*>(t + swz(o));
-      const uint4 b = *reinterpret_cast<const uint4*>(t + swz(o + 8 * D));
-      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t A[4];
-        C::halves(wa[j], A[0], A[2]);
-        C::halves(wb[j], A[1], A[3]);
-        const int ks = 4 * v + j;
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) mma_f16_16816(sc[mt], A, qf[p][2 * ks], qf[p][2 * ks + 1]);
-      }
-    }
-  }
-}
-
-// o = O^T of the tile with weights p (the layout of sc): o[mt][0, 1] dim
-// gq D / 8 + 2 mt of columns 2 c4 and 2 c4 + 1; o[mt][2, 3] the next dim
-template <typename C, int D, int S, int PARTS>
-HILS_DI void tile_values(const uint8_t* t, int gq, int c4, const float (&p)[S / 16][4], float (&o)[D / 16][4]) {
-  constexpr int W = D / 32;  // words of a thread's part of a key
-#pragma unroll
-  for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-#pragma unroll
-  for (int kk = 0; kk < S / 16; ++kk) {
-    uint32_t b0[PARTS], b1[PARTS];
-    const uint32_t h0 = pack_f16x2(p[kk][0], p[kk][1]), h1 = pack_f16x2(p[kk][2], p[kk][3]);
-    b0[0] = movmatrix_trans16(h0);
-    b1[0] = movmatrix_trans16(h1);
-    if (PARTS == 2) {
-      b0[PARTS - 1] = movmatrix_trans16(rest_f16x2(p[kk][0], p[kk][1], h0));
-      b1[PARTS - 1] = movmatrix_trans16(rest_f16x2(p[kk][2], p[kk][3], h1));
-    }
-    uint32_t w[4][W];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t* a = t + swz((16 * kk + 2 * c4 + (e & 1) + 8 * (e >> 1)) * D + gq * (D / 8));
-      if (W == 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(a);
-        w[e][0] = x.x, w[e][1] = x.y, w[e][W - 2] = x.z, w[e][W - 1] = x.w;
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 2) {
+        const float2 f = bf16x2_to_f32x2(r[i]);
+        x[v * PER + 2 * i] = f.x;
+        x[v * PER + 2 * i + 1] = f.y;
       } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(a);
-        w[e][0] = x.x, w[e][1] = x.y;
+        x[v * PER + i] = __uint_as_float(r[i]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      uint32_t A[4];
-      C::halves(C::pair01(w[0][j], w[1][j]), A[0], A[1]);
-      C::halves(C::pair01(w[2][j], w[3][j]), A[2], A[3]);
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) mma_f16_16816(o[2 * j], A, b0[q], b1[q]);
-      C::halves(C::pair23(w[0][j], w[1][j]), A[0], A[1]);
-      C::halves(C::pair23(w[2][j], w[3][j]), A[2], A[3]);
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) mma_f16_16816(o[2 * j + 1], A, b0[q], b1[q]);
-    }
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  // the row's four parts
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
 }
 
 // reductions over the 8 threads that share a column (lanes differing in gq)
@@ -225,15 +221,254 @@ HILS_DI float column_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 8);
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
-// 2^x (0 for -inf)
-HILS_DI float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-HILS_DI float exp_neg(float x) { return exp2_fast(x * kLog2e); }
-// 2^15 e^x, x <= 0
-constexpr float kWeight1 = 32768.f;
-HILS_DI float weight_of(float x) { return exp2_fast(fmaf(x, kLog2e, 15.f)); }
+
+// ------------------------------------------------------------- 8-bit products ---
+// Column n: head n / 2, digit n & 1; weights (hi, lo); queries (hi, mid), then (lo, none).
+template <int D, int S, int G>
+struct DigitOps {
+  using C = CodeI8;
+  static_assert(G <= 4, "one block of columns");
+  static constexpr int R = 1;  // heads of a thread
+  static constexpr float kOne = C::kOne, kLog2One = C::kLog2One;  // weights are given times kOne
+  static HILS_DI int head(int, int c4) { return c4; }
+  static constexpr int Q = 2;
+  struct Query {
+    uint32_t w[R][Q][D / 16];
+    float up[R];  // what a score of head(r, c4) is multiplied by
+  };
+  // the head whose row a thread gives to make_query
+  static HILS_DI int row_head(int gq) { return gq >> 1; }
+  template <typename T>
+  static HILS_DI void make_query(const RawRow<T, D>& raw, int gq, int c4, Query& q) {
+    float x[D / 4], down = 0.f, up = 0.f;
+    const unsigned top = row_values<T, D>(raw, x);
+    if (top != 0u && top < 0x7f800000u) C::row_factor(__uint_as_float(top), down, up);
+    if (top >= 0x7f800000u) up = __uint_as_float(0x7fc00000u);  // a row with an infinity or NaN scores NaN
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const float y[4] = {x[4 * i] * down, x[4 * i + 1] * down, x[4 * i + 2] * down, x[4 * i + 3] * down};
+      uint32_t w[Q];
+      C::query4(y, gq & 1, w);
+#pragma unroll
+      for (int d = 0; d < Q; ++d) q.w[0][d][i] = w[d];
+    }
+    q.up[0] = __shfl_sync(0xffffffffu, up, 8 * c4);
+  }
+  static HILS_DI void scores(const uint8_t* t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
+    constexpr int V = D / 64;
+#pragma unroll
+    for (int mt = 0; mt < S / 16; ++mt) {
+      uint32_t w[2][4 * V];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const uint4 x = *reinterpret_cast<const uint4*>(t + at.k[v][hi] + 16 * mt * D);
+          w[hi][4 * v] = x.x, w[hi][4 * v + 1] = x.y, w[hi][4 * v + 2] = x.z, w[hi][4 * v + 3] = x.w;
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        int d[Q][4];
+#pragma unroll
+        for (int ks = 0; ks < 2 * V; ++ks) {
+          const uint32_t A[4] = {w[0][2 * ks], w[1][2 * ks], w[0][2 * ks + 1], w[1][2 * ks + 1]};
+#pragma unroll
+          for (int x = 0; x < Q; ++x) {
+            if (ks == 0) mma_8bit_first(d[x], A, q.w[r][x][0], q.w[r][x][1]);
+            else mma_8bit(d[x], A, q.w[r][x][2 * ks], q.w[r][x][2 * ks + 1]);
+          }
+        }
+        sc[r][2 * mt] = C::score(d[0][0], d[0][1], d[Q - 1][0]);
+        sc[r][2 * mt + 1] = C::score(d[0][2], d[0][3], d[Q - 1][2]);
+      }
+    }
+  }
+  static HILS_DI void values(const uint8_t* t, const TileOffsets<D>& at, int gq, const float (&p)[R][S / 8],
+                             float (&o)[R][D / 8]) {
+    // P^T fragments.  A 16-bit element holds the two digits of a weight; the
+    // transpose leaves a thread (gq, c4) with head gq / 2 of keys 2 c4 and 2 c4 + 1
+    // (+ 8 if gq is odd); it keeps the digit of its column and gets its
+    // neighbour's other keys for it.
+    uint32_t b[R][S / 16];
+    const bool odd = gq & 1;
+    const uint32_t keep_s = odd ? 0x6420u : 0x7531u, send_s = odd ? 0x7531u : 0x6420u;
+    const uint32_t b0_s = odd ? 0x1054u : 0x5410u, b1_s = odd ? 0x3276u : 0x7632u;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int kk = 0; kk < S / 32; ++kk) {
+        const uint32_t x = movmatrix_trans16(C::digits2(p[r][4 * kk], p[r][4 * kk + 1]));
+        const uint32_t y = movmatrix_trans16(C::digits2(p[r][4 * kk + 2], p[r][4 * kk + 3]));
+        const uint32_t keep = __byte_perm(x, y, keep_s);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(x, y, send_s), 4);
+        b[r][2 * kk] = __byte_perm(keep, got, b0_s);
+        b[r][2 * kk + 1] = __byte_perm(keep, got, b1_s);
+      }
+    constexpr int W = D / 32;  // words of a thread's part of a key
+    int d[R][D / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < S / 32; ++kk) {
+      uint32_t w[2][4][W];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint8_t* a = t + at.v[e] + 16 * (2 * kk + half) * D;
+          if (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(a);
+            w[half][e][0] = x.x, w[half][e][1] = x.y, w[half][e][W - 2] = x.z, w[half][e][W - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(a);
+            w[half][e][0] = x.x, w[half][e][1] = x.y;
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        // bytes of four keys of one dim in a word, for the two groups of keys
+        uint32_t z[2][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t t0 = __byte_perm(w[half][0][j], w[half][1][j], 0x5140),
+                         t1 = __byte_perm(w[half][2][j], w[half][3][j], 0x5140),
+                         t2 = __byte_perm(w[half][0][j], w[half][1][j], 0x7362),
+                         t3 = __byte_perm(w[half][2][j], w[half][3][j], 0x7362);
+          z[half][0] = __byte_perm(t0, t1, 0x5410);
+          z[half][1] = __byte_perm(t0, t1, 0x7632);
+          z[half][2] = __byte_perm(t2, t3, 0x5410);
+          z[half][3] = __byte_perm(t2, t3, 0x7632);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t A[4] = {z[0][2 * m], z[0][2 * m + 1], z[1][2 * m], z[1][2 * m + 1]};
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (kk == 0) mma_8bit_first(d[r][2 * j + m], A, b[r][0], b[r][1]);
+            else mma_8bit(d[r][2 * j + m], A, b[r][2 * kk], b[r][2 * kk + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        o[r][2 * mt] = C::join(d[r][mt][0], d[r][mt][1]);
+        o[r][2 * mt + 1] = C::join(d[r][mt][2], d[r][mt][3]);
+      }
+  }
+};
+
+// ------------------------------------------------------------ half precision ---
+template <typename C, int D, int S, int G, int PARTS = 2>
+struct HalfOps {
+  static constexpr int R = 2;
+  static constexpr float kOne = 32768.f, kLog2One = 15.f;
+  static HILS_DI int head(int r, int c4) { return 2 * c4 + r; }
+  struct Query {
+    uint32_t w[PARTS][D / 8];  // nearest half (and rest)
+    float up[R];
+  };
+  static HILS_DI int row_head(int gq) { return gq; }
+  template <typename T>
+  static HILS_DI void make_query(const RawRow<T, D>& raw, int, int c4, Query& q) {
+    float x[D / 4];
+    const unsigned top = row_values<T, D>(raw, x);
+    // the power of two that brings the largest element into [2^14, 2^15); 2^14
+    // for a row that is zero or not finite
+    unsigned ex = top >> 23;
+    ex = top == 0 || ex == 255 ? 127 : max(ex, 15u);
+    const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex - 14u) << 23);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const float a = x[4 * ks] * down, b = x[4 * ks + C::kX1] * down, c = x[4 * ks + C::kY0] * down,
+                  d = x[4 * ks + 3] * down;
+      q.w[0][2 * ks] = pack_f16x2(a, b);
+      q.w[0][2 * ks + 1] = pack_f16x2(c, d);
+      if (PARTS == 2) {
+        q.w[PARTS - 1][2 * ks] = rest_f16x2(a, b, q.w[0][2 * ks]);
+        q.w[PARTS - 1][2 * ks + 1] = rest_f16x2(c, d, q.w[0][2 * ks + 1]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) q.up[r] = __shfl_sync(0xffffffffu, up, 4 * (2 * c4 + r));
+  }
+  static HILS_DI void scores(const uint8_t* t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
+    constexpr int V = D / 64;
+#pragma unroll
+    for (int mt = 0; mt < S / 16; ++mt) {
+      float d[4];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint4 a = *reinterpret_cast<const uint4*>(t + at.k[v][0] + 16 * mt * D),
+                    b = *reinterpret_cast<const uint4*>(t + at.k[v][1] + 16 * mt * D);
+        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t A[4];
+          C::halves(wa[j], A[0], A[2]);
+          C::halves(wb[j], A[1], A[3]);
+          const int ks = 4 * v + j;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            if (ks == 0 && p == 0) mma_f16_16816_first(d, A, q.w[p][0], q.w[p][1]);
+            else mma_f16_16816(d, A, q.w[p][2 * ks], q.w[p][2 * ks + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) sc[r][2 * mt] = d[r], sc[r][2 * mt + 1] = d[2 + r];
+    }
+  }
+  static HILS_DI void values(const uint8_t* t, const TileOffsets<D>& at, int, const float (&p)[R][S / 8],
+                             float (&o)[R][D / 8]) {
+    constexpr int W = D / 32;  // words of a thread's part of a key
+    float d[D / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < S / 16; ++kk) {
+      uint32_t b0[PARTS], b1[PARTS];
+      const uint32_t h0 = pack_f16x2(p[0][2 * kk], p[1][2 * kk]), h1 = pack_f16x2(p[0][2 * kk + 1], p[1][2 * kk + 1]);
+      b0[0] = movmatrix_trans16(h0);
+      b1[0] = movmatrix_trans16(h1);
+      if (PARTS == 2) {
+        b0[PARTS - 1] = movmatrix_trans16(rest_f16x2(p[0][2 * kk], p[1][2 * kk], h0));
+        b1[PARTS - 1] = movmatrix_trans16(rest_f16x2(p[0][2 * kk + 1], p[1][2 * kk + 1], h1));
+      }
+      uint32_t w[4][W];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint8_t* a = t + at.v[e] + 16 * kk * D;
+        if (W == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(a);
+          w[e][0] = x.x, w[e][1] = x.y, w[e][W - 2] = x.z, w[e][W - 1] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(a);
+          w[e][0] = x.x, w[e][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        uint32_t A[4];
+        C::halves(C::pair01(w[0][j], w[1][j]), A[0], A[1]);
+        C::halves(C::pair01(w[2][j], w[3][j]), A[2], A[3]);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          if (kk == 0 && q == 0) mma_f16_16816_first(d[2 * j], A, b0[q], b1[q]);
+          else mma_f16_16816(d[2 * j], A, b0[q], b1[q]);
+        }
+        C::halves(C::pair23(w[0][j], w[1][j]), A[0], A[1]);
+        C::halves(C::pair23(w[2][j], w[3][j]), A[2], A[3]);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          if (kk == 0 && q == 0) mma_f16_16816_first(d[2 * j + 1], A, b0[q], b1[q]);
+          else mma_f16_16816(d[2 * j + 1], A, b0[q], b1[q]);
+        }
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+      for (int r = 0; r < R; ++r) o[r][2 * mt] = d[mt][r], o[r][2 * mt + 1] = d[mt][2 + r];
+  }
+};
 
 }  // namespace hils

@@ -304,23 +304,26 @@ def _t(t: torch.Tensor, shape, dtype, device) -> int:
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, heads: int, cfg: Config, n: int, device) -> int:
-    """Address of rows [n, heads, d] whose heads are contiguous (any row and head strides)."""
-    assert t.shape == (n, heads, cfg.head_dim) and t.dtype is _dtype(cfg) and t.device == device, (
-        f"expected {_dtype(cfg)} rows [{n}, {heads}, {cfg.head_dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    assert t.stride(2) == 1, "the elements of a head must be contiguous"
-    return t.data_ptr()
+def _rows(t: torch.Tensor, shape, dtype, device):
+    """Address, row stride and head stride of rows [n, heads, d] whose heads are contiguous."""
+    row, head, one = t.stride() if t.ndim == 3 else (0, 0, 0)
+    assert one == 1 and t.shape == shape and t.dtype is dtype and t.device == device, (
+        f"expected {dtype} rows {tuple(shape)} with contiguous heads on {device}, "
+        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), row, head
 
 
 def _launch(device, fn, *args, stream):
     """fn(*args, stream) on the tensors' device (its current stream if None)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() != device.index:
+    at = device.index
+    raw = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() != at:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+            st = fn(*args, raw)
     else:
-        _check(fn(*args, stream.cuda_stream))
+        st = fn(*args, raw)
+    if st != HILS_OK:
+        _check(st)
 
 
 def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) -> Cache:
@@ -379,18 +382,19 @@ def hils_cache_append(cfg: Config, pg: Paged, cache: Cache, k, v, q=None, q_out=
     """Rotate and append: k, v [n, Hkv, d], q and q_out [n, Hq, d] (views with contiguous heads);
     row_start [B + 1] and positions [n] int32."""
     _cache_fits(cfg, pg, cache)
-    dev, n, hkv = cache.device, k.shape[0], cfg.n_kv_heads
-    r = Rows(_rows(k, hkv, cfg, n, dev), _rows(v, hkv, cfg, n, dev), None, None, k.stride(0), k.stride(1),
-             v.stride(0), v.stride(1), 0, 0, 0, 0, None, None, n)
+    dev, el, n, d = cache.device, cache.elements, k.shape[0], cfg.head_dim
+    shape = (n, cfg.n_kv_heads, d)
+    k, k_row, k_head = _rows(k, shape, el, dev)
+    v, v_row, v_head = _rows(v, shape, el, dev)
+    qa = q_row = q_head = oa = o_row = o_head = 0
     if q is not None:
         assert q_out is not None, "q needs q_out"
-        r.q, r.q_out = _rows(q, cfg.n_q_heads, cfg, n, dev), _rows(q_out, cfg.n_q_heads, cfg, n, dev)
-        r.q_row, r.q_head = q.stride(0), q.stride(1)
-        r.q_out_row, r.q_out_head = q_out.stride(0), q_out.stride(1)
-    if row_start is not None:
-        r.row_start = _t(row_start, (cfg.batch + 1,), torch.int32, dev)
-    if positions is not None:
-        r.positions = _t(positions, (n,), torch.int32, dev)
+        shape = (n, cfg.n_q_heads, d)
+        qa, q_row, q_head = _rows(q, shape, el, dev)
+        oa, o_row, o_head = _rows(q_out, shape, el, dev)
+    start = None if row_start is None else _t(row_start, (cfg.batch + 1,), torch.int32, dev)
+    pos = None if positions is None else _t(positions, (n,), torch.int32, dev)
+    r = Rows(k, v, qa, oa, k_row, k_head, v_row, v_head, q_row, q_head, o_row, o_head, start, pos, n)
     if rope is not None:
         assert rope.device == dev, "the angle tables are on another device than the cache"
         rope = ctypes.byref(rope)

@@ -358,7 +358,7 @@ typedef struct {
  * outside [1, L_max] or below its number of new rows is skipped; a page outside
  * the pool is not written; a row whose position lies outside the tables is
  * stored unrotated.  Rows of no sequence (before row_start[0], from
- * row_start[B] on) are neither read nor written.  No page may belong to two
+ * row_start[B] on) are never written.  No page may belong to two
  * chunks that one call writes.  The value rows, scales and codes repeat bit
  * for bit. */
 hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,

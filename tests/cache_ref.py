@@ -96,21 +96,22 @@ class RefCache:
 
 def summaries(k, q_lmk, scale):
     """k [Hkv, C, S, d], q_lmk [Hq, C, d] float64 -> k_sum [Hq, C, d], b_sum [Hq, C], sum p |k|, and
-    2^-40 (largest p) sum |k|."""
+    (largest p) sum |k|."""
     G = q_lmk.shape[0] // k.shape[0]
     kk = k.repeat_interleave(G, dim=0)
     p = torch.softmax(torch.einsum("hcd,hcsd->hcs", q_lmk, kk) * scale, dim=-1)
     return (torch.einsum("hcs,hcsd->hcd", p, kk), torch.special.entr(p).sum(dim=-1),
-            torch.einsum("hcs,hcsd->hcd", p, kk.abs()), p.amax(dim=-1, keepdim=True) * kk.abs().sum(dim=2) * 2.0 ** -40)
+            torch.einsum("hcs,hcsd->hcd", p, kk.abs()), p.amax(dim=-1, keepdim=True) * kk.abs().sum(dim=2))
 
 
 def attend(q, k, v, lists, s_sel, S, W, scale):
     """One token: q [Hq, d], k, v [Hkv, L, d], lists [Hkv][..] of chunks (with -1), s_sel [Hq, K], all float64.
-    -> out [Hq, d], sum w |v| [Hq, d], 2^-40 sum (largest w of the chunk) |v|, and the largest sum |q_e k_e| scale over
-    the keys it reads."""
+    -> out [Hq, d], sum w |v| [Hq, d], sum (largest w of the chunk) |v|, and the largest sum |q_e k_e| scale and
+    max |q| sum |k_e| scale over the keys it reads."""
     Hq, Hkv, L = q.shape[0], k.shape[0], k.shape[1]
     G, first = Hq // Hkv, max(0, (L - 1) // S - W // S + 1) * S
     out, mag, low, big = torch.empty_like(q), torch.empty_like(q), torch.zeros_like(q), 0.0
+    wide = 0.0
     for h in range(Hq):
         g = h // G
         logit = k[g] @ q[h] * scale
@@ -131,6 +132,8 @@ def attend(q, k, v, lists, s_sel, S, W, scale):
         own = L - first
         edges = list(range(0, own, S)) + list(range(own, len(w) + 1, S))
         for a, z in zip(edges, edges[1:]):
-            low[h] += w[a:z].max() * vals[a:z].abs().sum(dim=0) * 2.0 ** -40
-        big = max(big, float((torch.cat(keys).abs() @ q[h].abs()).max() * scale))
-    return out, mag, low, big
+            low[h] += w[a:z].max() * vals[a:z].abs().sum(dim=0)
+        keys = torch.cat(keys).abs()
+        big = max(big, float((keys @ q[h].abs()).max() * scale))
+        wide = max(wide, float(keys.sum(dim=1).max() * q[h].abs().max() * scale))
+    return out, mag, low, big, wide

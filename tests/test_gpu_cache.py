@@ -7,15 +7,20 @@ rotated queries are defined by float32 operations in a given order: equal bits.
 For summaries and attention let mag = sum of weight * |value| (from the model):
   * an output element is a weighted sum of at most n held values.  The logits
     are float32 sums of d products: off by at most (d + 4) 2^-24 big, big =
-    max sum |q_e k_e| scale (the two scale factors round once each).  Float32
-    queries are held as two halves, off by 2^-22 of themselves, which a factor
-    of two covers.  A weight is off by twice that (its numerator and its sum),
-    and by 2^-20 for exp, log and the quotient;
-  * float32 inputs: weights are held to 2^-22, sums of S products, then of units:
-    (S + n / S + 16) 2^-24;
-  * no weight is resolved below 2^-40 of its chunk's largest (`low`);
-  * bf16 inputs: weights round to half precision (2^-11), and the result to
-    bf16 (2^-8 of itself).
+    max sum |q_e k_e| scale (the two scale factors round once each).  A weight is
+    off by twice that (its numerator and its sum), and by 2^-20 for exp, log
+    and the quotient; sums of S products, then of units: (S + n / S + 16) 2^-24;
+  * float32 inputs: queries are held as two halves, within 2^-22 of themselves,
+    which a factor of two on the logits' bound covers; weights within 2^-22, or
+    2^-40 of the largest of their chunk (low = sum of that largest * |value|);
+  * bf16 inputs, int8 codes: queries within 1.02 2^-24 of their row's largest
+    element (fixed point, half a step is 1 / 16646144), so a logit within that
+    times wide = max |q| sum |k_e| scale; weights within 1.02 2^-16 of their
+    chunk's largest (half a step is 1 / 65024); the result rounds to bf16 (2^-8
+    of itself);
+  * bf16 inputs, e4m3 codes: queries exact, or within 2^-17 of their row's largest
+    element (two e4m3 numbers, the largest in [2^7, 2^8), the smallest step
+    2^-9); weights within 2^-8 of themselves (2^-4 twice), or 2^-18 of the largest.
 """
 import math
 
@@ -31,14 +36,21 @@ DEV = "cuda:0"
 BF, F32, I8, E4 = torch.bfloat16, torch.float32, torch.int8, torch.float8_e4m3fn
 
 
-def weights_off(dtype, d, S, n, big):
-    """Relative error of a weighted sum's terms (see above)."""
+FIXED_Q, FIXED_P = 1.02 * 2.0 ** -24, 1.02 * 2.0 ** -16
+
+
+def weights_off(dtype, code, d, S, n, big, wide):
+    """Relative error of a weighted sum's terms, and the part of each chunk's largest weight that they resolve."""
     off = 2 * 2 * (d + 4) * 2.0 ** -24 * big + 2.0 ** -20 + (S + n / S + 16) * 2.0 ** -24
-    return off + (2.0 ** -22 if dtype is F32 else 2.0 ** -11)
+    if code is None:
+        return off, 0.0
+    if dtype is F32:
+        return off + 2.0 ** -22, 2.0 ** -40
+    return (off + 2 * FIXED_Q * wide, FIXED_P) if code is I8 else (off + 2 * 2.0 ** -17 * wide + 2.0 ** -8, 2.0 ** -18)
 
 
-def out_off(dtype, got, want, mag, low, rel):
-    tol = mag * rel + low + (want.abs() * 2.0 ** -8 if dtype is BF else want.abs() * 2.0 ** -24)
+def out_off(dtype, got, want, mag, low, off):
+    tol = mag * off[0] + low * off[1] + (want.abs() * 2.0 ** -8 if dtype is BF else want.abs() * 2.0 ** -24)
     return ((got.double().cpu() - want).abs() - tol).max().item()
 
 
@@ -123,10 +135,10 @@ class Case:
     def check_attention(self, lens, q, idx, s_sel, out, accepted=None):
         for b, L in enumerate(lens):
             k, v = self.ref.values(0, b, L), self.ref.values(1, b, L)
-            want, mag, low, big = attend(q[b].double(), k, v, (idx if accepted is None else accepted)[b].tolist(),
+            want, mag, low, big, wide = attend(q[b].double(), k, v, (idx if accepted is None else accepted)[b].tolist(),
                                     s_sel[b].double(), self.S, self.W, self.scale)
             n = self.K * self.S + self.W
-            rel = weights_off(self.dtype, self.d, self.S, n, big)
+            rel = weights_off(self.dtype, self.code, self.d, self.S, n, big, wide)
             assert out_off(self.dtype, out[b], want, mag, low, rel) <= 0, (b, L)
 
 
@@ -434,11 +446,14 @@ def check_summaries(c, lens, first, q_lmk, k_sum, b_sum, blank_k, blank_b):
         ql = q_lmk(b, range(first[b], C))
         want, ent, mag, low = summaries(k, ql, c.scale)
         big = float((k.abs().amax(dim=2).repeat_interleave(c.Hq // c.Hkv, 0) * ql.abs()).sum(-1).max() * c.scale)
-        rel = weights_off(c.dtype, c.d, c.S, c.S, big)
+        wide = float((k.abs().sum(dim=3).amax(dim=2).repeat_interleave(c.Hq // c.Hkv, 0) * ql.abs().amax(dim=2)).max() * c.scale)
+        rel = weights_off(c.dtype, c.code, c.d, c.S, c.S, big, wide)
         assert out_off(c.dtype, k_sum[b][:, first[b]:C], want, mag, low, rel) <= 0, b
         # H(p) = -sum p log p: each p off by `eps` of itself moves it by at most eps (H + 1), and log and exp of
-        # arguments up to `big` by 2^-22 of them
+        # arguments up to `big` by 2^-22 of them; the entropy's p are not rounded to digits
         eps = 2 * 2 * (c.d + 4) * 2.0 ** -24 * big + 2.0 ** -20 + (c.S + 16) * 2.0 ** -24
+        if c.dtype is BF and c.code is not None:
+            eps += 2 * (FIXED_Q if c.code is I8 else 2.0 ** -17) * wide
         off = (b_sum[b][:, first[b]:C].double().cpu() - ent).abs()
         assert (off <= eps * (ent + 1) + 2.0 ** -22 * big).all(), (b, off.max())
 
