@@ -355,12 +355,128 @@ HILS_DI void row8(const __nv_bfloat16* p, float (&x)[8]) {
   }
 }
 
+// 16 keys of a tail, with the arithmetic of float32: scores sc[r][hi] of key
+// gq + 8 hi and head Ops::head(r, c4), and acc += weights . values (dims gq D / 8 + x).
+// float32 configurations: on CUDA cores.
+template <typename T, typename Ops, int D>
+struct TailSlice {
+  static constexpr int R = Ops::R, N8 = D / 8;
+  const T *kt, *vt, *q0;
+  int nk, heads, gq, c4;
+  HILS_DI void load(const T* kt_, const T* vt_, const T* q0_, int nk_, int G, int gq_, int c4_) {
+    kt = kt_, vt = vt_, q0 = q0_, nk = nk_, heads = G, gq = gq_, c4 = c4_;
+  }
+  HILS_DI void scores(float (&sc)[R][2]) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 8) {
+      float k0[8], k1[8];
+      row8(kt + min(gq, nk - 1) * D + e, k0);
+      row8(kt + min(gq + 8, nk - 1) * D + e, k1);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float qa[8];
+        row8(q0 + min(Ops::head(r, c4), heads - 1) * D + e, qa);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          sc[r][0] = fmaf(k0[x], qa[x], sc[r][0]);
+          sc[r][1] = fmaf(k1[x], qa[x], sc[r][1]);
+        }
+      }
+    }
+  }
+  HILS_DI void add_values(const float (&p)[R][2], float (&acc)[R][N8]) const {
+#pragma unroll 4
+    for (int k = 0; k < nk; ++k) {
+      float w[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, k < 8 ? p[r][0] : p[r][1], 4 * (k & 7) + c4);
+#pragma unroll
+      for (int e = 0; e < N8; e += 8) {
+        float v[8];
+        row8(vt + k * D + gq * N8 + e, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) acc[r][e + x] = fmaf(w[r], v[x], acc[r][e + x]);
+      }
+    }
+  }
+};
+HILS_DI float bf16_part(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+// bf16 configurations: bf16 mma.sync, all of the slice's loads in flight at once.
+// Weights are the sum of two bf16 numbers (within 2^-17 of themselves), as two
+// products, or where a thread has one head, in the two columns of that head.
+template <typename Ops, int D>
+struct TailSlice<__nv_bfloat16, Ops, D> {
+  using T = __nv_bfloat16;
+  static constexpr int R = Ops::R, N8 = D / 8, Q4 = D / 32, V4 = N8 / 8;
+  uint4 k[2][Q4], q[Q4], v[4][V4];
+  HILS_DI static uint32_t word(const uint4* x, int i) {
+    const uint4& w = x[i >> 2];
+    return (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w;
+  }
+  HILS_DI void load(const T* kt, const T* vt, const T* q0, int nk, int G, int gq, int c4) {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const int h = Ops::row_head(gq);
+#pragma unroll
+    for (int x = 0; x < Q4; ++x) {
+      k[0][x] = __ldg(reinterpret_cast<const uint4*>(kt + min(gq, nk - 1) * D + c4 * (D / 4)) + x);
+      k[1][x] = __ldg(reinterpret_cast<const uint4*>(kt + min(gq + 8, nk - 1) * D + c4 * (D / 4)) + x);
+      q[x] = h < G ? __ldg(reinterpret_cast<const uint4*>(q0 + h * D + c4 * (D / 4)) + x) : none;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = 2 * c4 + (e & 1) + 8 * (e >> 1);
+#pragma unroll
+      for (int x = 0; x < V4; ++x)
+        v[e][x] = key < nk ? __ldg(reinterpret_cast<const uint4*>(vt + key * D + gq * N8) + x) : none;
+    }
+  }
+  HILS_DI void scores(float (&sc)[R][2]) const {
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t A[4] = {word(k[0], 2 * ks), word(k[1], 2 * ks), word(k[0], 2 * ks + 1), word(k[1], 2 * ks + 1)};
+      mma_bf16_16816(d, A, word(q, 2 * ks), word(q, 2 * ks + 1));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) sc[r][0] = d[r], sc[r][1] = d[2 + r];
+  }
+  HILS_DI void add_values(const float (&p)[R][2], float (&acc)[R][N8]) const {
+    uint32_t b[2][R];
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+      const float x0 = p[0][hi], x1 = R == 2 ? p[R - 1][hi] : x0 - bf16_part(x0);
+      b[hi][0] = movmatrix_trans16(pack_bf16x2(x0, x1));
+      if (R == 2) b[hi][R - 1] = movmatrix_trans16(pack_bf16x2(x0 - bf16_part(x0), x1 - bf16_part(x1)));
+    }
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      const uint32_t w[4] = {word(v[0], mt), word(v[1], mt), word(v[2], mt), word(v[3], mt)};
+      const uint32_t A[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                             __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < R; ++x) mma_bf16_16816(d, A, b[0][x], b[1][x]);
+      if (R == 2) {
+        acc[0][2 * mt] += d[0], acc[R - 1][2 * mt] += d[1];
+        acc[0][2 * mt + 1] += d[2], acc[R - 1][2 * mt + 1] += d[3];
+      } else {
+        acc[0][2 * mt] += d[0] + d[1];
+        acc[0][2 * mt + 1] += d[2] + d[3];
+      }
+    }
+  }
+};
+
 constexpr int kMaxUnits = 64 + 32;  // K list entries, W / S window chunks
 constexpr int kMaxWarps = 12;       // 16 KB of buffers each at d = 128, S = 64, up to 170 registers a thread
 
 // A cluster of CTAs serves one (sequence, KV head).  Units, dealt to the
-// cluster's warps in turn: 16-key slices of the incomplete chunk (in float32 on
-// CUDA cores, from the tail), then the window's complete chunks and the chosen
+// cluster's warps in turn: 16-key slices of the incomplete chunk (from the tail),
+// then the window's complete chunks and the chosen
 // chunks (tiles of codes).  Each warp folds its units with a running maximum per
 // head, the CTA its warps, and the cluster its CTAs through distributed shared
 // memory: one launch, no workspace, a fixed order of adding.
@@ -488,30 +604,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   look_ahead(first);
 
   for (; i < n_tail; i += step) {
-    // keys [16 i, 16 i + 16) of the incomplete chunk, in float32
+    // keys [16 i, 16 i + 16) of the incomplete chunk, as they are in the tail
     const long long off = tail_off(s, b, g, cur) + 16 * i * D;
     const T* kt = (const T*)cv.k_tail + off;
     const T* vt = (const T*)cv.v_tail + off;
     const int nk = min(16, part - 16 * i);
     float sc[R][2];  // keys gq and gq + 8
-#pragma unroll
-    for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = 0.f;
-#pragma unroll 4
-    for (int e = 0; e < D; e += 8) {
-      float k0[8], k1[8];
-      row8(kt + min(gq, nk - 1) * D + e, k0);
-      row8(kt + min(gq + 8, nk - 1) * D + e, k1);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float qa[8];
-        row8(q0 + min(Ops::head(r, c4), G - 1) * D + e, qa);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          sc[r][0] = fmaf(k0[x], qa[x], sc[r][0]);
-          sc[r][1] = fmaf(k1[x], qa[x], sc[r][1]);
-        }
-      }
-    }
+    TailSlice<T, Ops, D> slice;
+    slice.load(kt, vt, q0, nk, G, gq, c4);
+    slice.scores(sc);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       sc[r][0] = gq < nk ? sc[r][0] * s.scale : -INFINITY;
@@ -526,21 +627,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
 #pragma unroll
       for (int x = 0; x < N8; ++x) acc[r][x] *= fo;
     }
-#pragma unroll 4
-    for (int k = 0; k < nk; ++k) {
-      float p[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) p[r] = __shfl_sync(0xffffffffu, k < 8 ? sc[r][0] : sc[r][1], 4 * (k & 7) + c4);
-#pragma unroll
-      for (int e = 0; e < N8; e += 8) {
-        float v[8];
-        row8(vt + k * D + gq * N8 + e, v);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) acc[r][e + x] = fmaf(p[r], v[x], acc[r][e + x]);
-      }
-    }
+    slice.add_values(sc, acc);
   }
 
   int n_done = 0;
