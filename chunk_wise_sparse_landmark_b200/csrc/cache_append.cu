@@ -4,8 +4,8 @@
 // The hyper.ai summary of arXiv 2607.02980 (HiLS-Attention), section 实验
 // (Experiments), counts what a decode step touches; codes of one byte with one
 // scale for each chunk and KV head halve it.  A block X (one chunk of one KV
-// head, S x d values) with A = max |x| is held as code = rn(x (M / A)), scale =
-// A / M, M = 127 (int8) or 448 (e4m3).  It needs the whole block's A, so a
+// head, S x d values) with A = max |x| is held as code = rn(x (1 / A * M)), scale
+// = A (1 / M), M = 127 (int8) or 448 (e4m3).  It needs the whole block's A, so a
 // chunk becomes codes when its last token arrives; its tokens wait in a tail in
 // the configuration's type, and what the cache holds does not depend on how
 // tokens were split over calls.
@@ -128,7 +128,7 @@ HILS_DI void rotate_raw(const RopeView& rp, const float (&co)[8], const float (&
 }
 
 // ------------------------------------------------------------------- codes ---
-// Eight codes of x by.  int8: |x by| <= 127 (1 + 2^-22), so adding 1.5 2^23 rounds
+// Eight codes of x by.  int8: |x by| <= 127 (1 + 2^-21), so adding 1.5 2^23 rounds
 // it to an integer of at most 127, in the low byte, to nearest even.
 template <int FMT>
 HILS_DI uint2 encode8(const float (&x)[8], float by) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
     if (off < 0) continue;
     const float A = __uint_as_float(top), M = max_code(FMT);
     const bool fine = top < 0x7f800000u, zero = fine && A < kTiny, held = fine && !zero;
-    const float by = held ? __fdiv_rn(M, A) : 0.f;
+    const float by = held ? __fmul_rn(__frcp_rn(A), M) : 0.f;
     uint8_t* page = (uint8_t*)pools[x] + off;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
       *reinterpret_cast<uint2*>(page + j * D + e1) = held ? encode8<FMT>(z1, by) : none;
     }
     if (tid == 0)
-      scales[x][off / (S * D)] = !fine ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(A, M);
+      scales[x][off / (S * D)] = !fine ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fmul_rn(A, 1.f / M);
   }
   if (FMT != kNative && whole && c == c0 && reads_tail) {  // every thread has read its tail rows (the barriers above)
     for (int cc = max(last - 1, c0 + 1); cc <= last; ++cc) {

@@ -290,8 +290,8 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
  * with one scale for each page and KV head, k_scale / v_scale [num_pages,
  * Hkv] (a block of S tokens and one head).  A block X of S x d values of
  * cfg->dtype with largest magnitude A is held as
- *   scale = A / M,  code = round_to_nearest_even(x * (M / A)),  M = 127 or 448
- * (float32 operations).  A block with A < 2^-110 is held as zeros (scale 0);
+ *   scale = A * (1 / M),  code = round_to_nearest_even(x * ((1 / A) * M)),
+ * M = 127 or 448 (each operation rounded to float32).  A block with A < 2^-110 is held as zeros (scale 0);
  * a block with an infinity or a NaN gets the scale NaN, so that whatever
  * reads it is NaN.
  *   A chunk becomes codes when its last token arrives.  Until then its tokens

@@ -36,8 +36,9 @@ def encode(block, code_type):
     top = x.abs().max()
     if top < TINY:
         return torch.zeros_like(x).to(code_type), 0.0
-    y = (x * (torch.tensor(m) / top)).clamp(-m, m)
-    return (y.round() if code_type is torch.int8 else y).to(code_type), float(top / torch.tensor(m))
+    one, m32 = torch.tensor(1.0), torch.tensor(m)
+    y = (x * ((one / top) * m32)).clamp(-m, m)
+    return (y.round() if code_type is torch.int8 else y).to(code_type), float(top * (one / m32))
 
 
 class RefCache:
