@@ -215,6 +215,8 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
   __shared__ int sh_b;
   __shared__ int sh_seq[kThreads / 2];
   __shared__ unsigned sh_top[2][kThreads / 32];
+  const unsigned long long zero = grid_begin();
+  behind(zero, cv), behind(zero, dv), behind(zero, nr), behind(zero, rp);
   const int tid = threadIdx.x, slot = tid % SLOTS;
   int e0, e1;  // the thread's groups of every row
   slot_groups(slot, rp.rot, e0, e1);
@@ -457,9 +459,8 @@ cudaError_t go_append(const Shape& s, const CacheView& cv, const DecView& dv, co
   mix.fewer = (int)few;
   mix.per = few ? (int)(many / few) + 1 : 1;
   mix.fewer_queries = qc <= kv;
-  cache_append_kernel<T, FMT, D, S>
-      <<<(unsigned)(kv + qc), kThreads, 0, st>>>(s, cv, dv, nr, rp, mix, lanes, ctx);
-  return cudaGetLastError();
+  return launch_overlapped(cache_append_kernel<T, FMT, D, S>, dim3((unsigned)(kv + qc)), kThreads, 0, 1, st, s, cv, dv,
+                           nr, rp, mix, lanes, ctx);
 }
 
 // ------------------------------------------------------------- reading back ---
@@ -494,6 +495,8 @@ template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView cv, DecView dv, T* __restrict__ k_out,
                                                               T* __restrict__ v_out, int out_rows, DevCtx ctx) {
   constexpr bool coded = sizeof(C) == 1;
+  const unsigned long long zero = grid_begin();
+  behind(zero, cv), behind(zero, dv);
   const int c = blockIdx.x, g = blockIdx.y >> 1, b = blockIdx.z, vals = blockIdx.y & 1;
   T* out = vals ? v_out : k_out;
   if (!out) return;
@@ -559,18 +562,17 @@ cudaError_t launch_cache_read(const Shape& s, const CacheView& cv, const DecView
                               int out_rows, cudaStream_t st, const DevCtx& ctx) {
   const int chunks = ((out_rows < s.N ? out_rows : s.N) + s.S - 1) / s.S;
   const dim3 grid(chunks, 2 * s.Hkv, s.B);
-#define HILS_GO(T, C) cache_read_kernel<T, C><<<grid, kThreads, 0, st>>>(s, cv, dv, (T*)k_out, (T*)v_out, out_rows, ctx)
+#define HILS_GO(T, C) \
+  return launch_overlapped(cache_read_kernel<T, C>, grid, kThreads, 0, 1, st, s, cv, dv, (T*)k_out, (T*)v_out, out_rows, ctx)
   if (s.dtype == 0) {
     if (cv.format == kI8) HILS_GO(float, int8_t);
-    else if (cv.format == kE4M3) HILS_GO(float, __nv_fp8_e4m3);
-    else HILS_GO(float, float);
-  } else {
-    if (cv.format == kI8) HILS_GO(__nv_bfloat16, int8_t);
-    else if (cv.format == kE4M3) HILS_GO(__nv_bfloat16, __nv_fp8_e4m3);
-    else HILS_GO(__nv_bfloat16, __nv_bfloat16);
+    if (cv.format == kE4M3) HILS_GO(float, __nv_fp8_e4m3);
+    HILS_GO(float, float);
   }
+  if (cv.format == kI8) HILS_GO(__nv_bfloat16, int8_t);
+  if (cv.format == kE4M3) HILS_GO(__nv_bfloat16, __nv_fp8_e4m3);
+  HILS_GO(__nv_bfloat16, __nv_bfloat16);
 #undef HILS_GO
-  return cudaGetLastError();
 }
 
 }  // namespace hils

@@ -98,6 +98,7 @@ HILS_DI void fetch_tile(void* dst, const CUtensorMap* map, int tile, uint64_t* b
   mbar_arrive_expect_tx(bar, S * D);
   tma_load_2d(dst, map, 0, tile * (S * D / 128), bar);
 }
+HILS_DI void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // pool tile (page Hkv + g) of chunk c of sequence b, or -1: outside the pool (reported)
 HILS_DI int dv_tile(const DecView& dv, const Shape& s, int b, int g, int c, const DevCtx& ctx, bool report) {
   const int p = c < dv.max_pages ? __ldg(dv.pages + (long long)b * dv.max_pages + c) : -1;
@@ -124,29 +125,38 @@ struct OpsOf<__nv_bfloat16, CodeI8, D, S, 4> {
   using type = DigitOps<D, S, 4>;
 };
 
-// sc (logits) -> weights kOne e^{x - top}: `top` the column's largest logit, `l`
-// the weights' sum (float32); zl, if wanted, the sum of weight * (x - top)
+// sc (scores) -> weights kOne e^{x - top} of the logits x = sc mul: `top` the
+// column's largest logit, `l` the weights' sum (float32); zl, if wanted, the sum of
+// weight * (x - top).  In the exponent mul log2 e is one factor and top one term,
+// so each weight is off by 2^-23 |x| more, and by no instruction of its own.
 template <typename Ops, int N>
 HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = nullptr) {
-  top = -INFINITY;
+  if (mul < 0.f) {  // (a scale of a pool that was filled elsewhere)
+    mul = -mul;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    sc[i] *= mul;
-    top = fmaxf(top, sc[i]);
+    for (int i = 0; i < N; ++i) sc[i] = -sc[i];
   }
-  top = column_max(top);
-  const float m = top == -INFINITY ? 0.f : top;
+  float m = sc[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, sc[i]);
+  m = column_max(m);
+  top = m * mul;
+  const float f = mul * kLog2e, c = m == -INFINITY ? 0.f : m * f;
   l = 0.f;
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float x = sc[i] - m;
-    sc[i] = exp2_fast(fmaf(x, kLog2e, Ops::kLog2One));
+    if (zl) {
+      const float x = fmaf(sc[i], f, -c);
+      sc[i] = exp2_fast(x + Ops::kLog2One);
+      z = fmaf(sc[i], x, z);
+    } else {
+      sc[i] = exp2_fast(fmaf(sc[i], f, Ops::kLog2One - c));
+    }
     l += sc[i];
-    if (zl) z += sc[i] * x;
   }
   l = column_sum(l);
-  if (zl) *zl = column_sum(z);
+  if (zl) *zl = column_sum(z) * kLn2;
 }
 
 // Warps take the chunks of all sequences in turn, so that short and long
@@ -158,8 +168,8 @@ constexpr int kSeqs = 512;
 
 template <typename T, typename C, int D, int S, int G>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel(
-    const __grid_constant__ CUtensorMap kmap, Shape s, CacheView cv, DecView dv, const T* __restrict__ q_lmk,
-    LmkStrides ls, const int* __restrict__ from, T* __restrict__ k_sum, float* __restrict__ b_sum, DevCtx ctx) {
+    const __grid_constant__ CUtensorMap kmap, Shape s, CacheView cv, DecView dv, const T* q_lmk,
+    LmkStrides ls, const int* from, T* k_sum, float* b_sum, DevCtx ctx) {
   using Ops = typename OpsOf<T, C, D, S, G>::type;
   constexpr int R = Ops::R, N8 = D / 8;
   constexpr int PER = kSeqs / (kWarps * 32);  // sequences of a thread
@@ -177,6 +187,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
     fence_barrier_init();
     fence_proxy_async_shared();
   }
+  const unsigned long long zero = grid_begin();
+  behind(zero, cv), behind(zero, dv), behind(zero, q_lmk), behind(zero, from);
+  if (lane == 0) fence_proxy_async_all();  // what earlier kernels stored is read by tile copies
   // chunks up to and with each sequence
   int n[PER], own = 0;
 #pragma unroll
@@ -219,13 +232,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
   const TileOffsets<D> at(gq, c4);
 
   // lane l: sequence, chunk, tile and scale of the warp's unit l of the next 32
-  int my_b = 0, my_c = 0, my_tile = -1;
+  int my_b = 0, my_c = 0, my_g = 0, my_tile = -1;
   float my_scale = 0.f;
   auto look_up = [&](long long u0) {
     const long long v = u0 + lane * step;
     my_tile = -1;
     if (v < units) {
       const int t = (int)(v / s.Hkv);
+      my_g = (int)(v - (long long)t * s.Hkv);
       int lo = 0, hi = nb - 1;  // the first sequence that ends behind t
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -234,32 +248,33 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
       }
       my_b = b0 + lo;
       my_c = firsts[lo] + t - (lo ? ends[lo - 1] : 0);
-      my_tile = dv_tile(dv, s, my_b, (int)(v % s.Hkv), my_c, ctx, true);
+      my_tile = dv_tile(dv, s, my_b, my_g, my_c, ctx, true);
     }
     my_scale = my_tile >= 0 ? __ldg(cv.k_scale + my_tile) : 0.f;
   };
   struct Unit {
-    int b, c, tile;
+    int b, g, c, tile;
     float ks;
   };
   auto unit_of = [&](int i) {
     Unit x;
     x.b = __shfl_sync(0xffffffffu, my_b, i & 31);
+    x.g = __shfl_sync(0xffffffffu, my_g, i & 31);
     x.c = __shfl_sync(0xffffffffu, my_c, i & 31);
     x.tile = __shfl_sync(0xffffffffu, my_tile, i & 31);
     x.ks = __shfl_sync(0xffffffffu, my_scale, i & 31);
     return x;
   };
   const int row = Ops::row_head(gq);
-  auto ask_query = [&](const Unit& x, long long v, RawRow<T, D>& raw) {
-    raw.load(row < G ? q_lmk + ls.of(x.b, (int)(v % s.Hkv) * G + row, x.c) : (const T*)nullptr, c4);
+  auto ask_query = [&](const Unit& x, RawRow<T, D>& raw) {
+    raw.load(row < G ? q_lmk + ls.of(x.b, x.g * G + row, x.c) : (const T*)nullptr, c4);
   };
   look_up(u);
   Unit now = unit_of(0);
   RawRow<T, D> raw;
   if (now.tile >= 0) {
     if (lane == 0) fetch_tile<D, S>(buf.a, &kmap, now.tile, &bar[0], ctx);
-    ask_query(now, u, raw);
+    ask_query(now, raw);
   }
   bool flying[2] = {now.tile >= 0, false};
   uint32_t phase[2] = {0u, 0u};
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
     }
     typename Ops::Query q;
     if (now.tile >= 0) Ops::template make_query<T>(raw, gq, c4, q);
-    if (next.tile >= 0) ask_query(next, u + step, raw);
+    if (next.tile >= 0) ask_query(next, raw);
     if (now.tile >= 0) {
       alive = mbar_wait(&bar[st], phase[st], ctx);
       if (!__all_sync(0xffffffffu, alive)) break;
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
       const uint8_t* t = st ? buf.b : buf.a;
       float sc[R][S / 8], o[R][N8], inv[R];
       Ops::scores(t, at, q, sc);
-      const long long h0 = (long long)now.b * s.Hq + (u % s.Hkv) * G;
+      const long long h0 = (long long)now.b * s.Hq + now.g * G;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = Ops::head(r, c4);
@@ -483,8 +498,7 @@ constexpr int kMaxWarps = 12;       // 16 KB of buffers each at d = 128, S = 64,
 template <typename T, typename C, int D, int S, int G>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Shape s,
-    const T* __restrict__ q, CacheView cv, DecView dv, const int32_t* __restrict__ idx,
-    const float* __restrict__ s_sel, T* __restrict__ out, int ncta, DevCtx ctx) {
+    const T* q, CacheView cv, DecView dv, const int32_t* idx, const float* s_sel, T* out, int ncta, DevCtx ctx) {
   using Ops = typename OpsOf<T, C, D, S, G>::type;
   constexpr int R = Ops::R, N8 = D / 8;
   extern __shared__ unsigned char smem_raw[];
@@ -494,6 +508,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   unsigned char* smem = align_1k(smem_raw);
   const int nwarp = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c4 = lane & 3;
   const int rank = blockIdx.x % ncta, g = (int)(blockIdx.x / ncta) % s.Hkv, b = (int)(blockIdx.x / ncta) / s.Hkv;
+  uint64_t* bar = bars[warp];
+  if (lane == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+  }
+  const unsigned long long zero = grid_begin();
+  behind(zero, cv), behind(zero, dv), behind(zero, q), behind(zero, idx), behind(zero, s_sel);
+  if (lane == 0) fence_proxy_async_all();  // what earlier kernels stored is read by tile copies
   int e0 = -1, e1 = -1;  // the list (warp 0), asked for beside the length
   if (warp == 0) {
     const int32_t* ir = idx + ((long long)b * s.Hkv + g) * s.K;
@@ -507,15 +533,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   }
   const int cur = (L - 1) / S, wc0 = max(0, cur - s.nw + 1);
   const int n_full = L / S - wc0, part = L % S, n_tail = (part + 15) / 16;
-  uint64_t* bar = bars[warp];
-  if (lane == 0) {
-    prefetch_tmap(&kmap);
-    prefetch_tmap(&vmap);
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
-    fence_barrier_init();
-    fence_proxy_async_shared();
-  }
   if (warp == 0) {
     // the live units: window chunks, then accepted list entries (the list form, common.cuh)
     bool bad;
@@ -760,9 +777,8 @@ cudaError_t go_summ(const Shape& s, const CacheView& cv, const DecView& dv, cons
   const int blocks = (s.B + kSeqs - 1) / kSeqs;
   const long long most = ((long long)(s.B < kSeqs ? s.B : kSeqs) * s.C * s.Hkv + kWarps - 1) / kWarps;
   const long long wave = (device_sm_count() * kCtasPerSm + blocks - 1) / blocks;
-  kern<<<dim3((unsigned)(wave < most ? wave : most), blocks), kWarps * 32, smem, st>>>(
-      km, s, cv, dv, (const T*)q_lmk, ls, from, (T*)k_sum, b_sum, ctx);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3((unsigned)(wave < most ? wave : most), blocks), kWarps * 32, smem, 1, st, km, s, cv,
+                           dv, (const T*)q_lmk, ls, from, (T*)k_sum, b_sum, ctx);
 }
 
 template <typename T, int D, int S, int G>
@@ -805,18 +821,8 @@ cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const De
   share = share < units ? share : units;
   int nwarp = (share + ncta - 1) / ncta;
   nwarp = nwarp > kMaxWarps ? kMaxWarps : nwarp;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)groups * ncta);
-  cfg.blockDim = dim3(nwarp * 32);
-  cfg.dynamicSmemBytes = sizeof(WarpBuffers<D, S>) * nwarp + 1024;
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = ncta;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = ncta > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, km, vm, s, (const T*)q, cv, dv, idx, s_sel, (T*)out, ncta, ctx);
+  return launch_overlapped(kern, dim3((unsigned)groups * ncta), nwarp * 32, sizeof(WarpBuffers<D, S>) * nwarp + 1024, ncta,
+                           st, km, vm, s, (const T*)q, cv, dv, idx, s_sel, (T*)out, ncta, ctx);
 }
 
 }  // namespace

@@ -184,13 +184,12 @@ struct RawRow {
       w[v] = row ? __ldg(reinterpret_cast<const uint4*>(row + c4 * N) + v) : make_uint4(0u, 0u, 0u, 0u);
   }
 };
-// its elements as float32, and the bits of the whole row's largest magnitude
+// its elements as float32
 template <typename T, int D>
-HILS_DI unsigned row_values(const RawRow<T, D>& raw, float (&x)[D / 4]) {
-  constexpr int N = D / 4, PER = 16 / sizeof(T);
-  unsigned top = 0;
+HILS_DI void row_values(const RawRow<T, D>& raw, float (&x)[D / 4]) {
+  constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-  for (int v = 0; v < N / PER; ++v) {
+  for (int v = 0; v < D / 4 / PER; ++v) {
     const uint32_t r[4] = {raw.w[v].x, raw.w[v].y, raw.w[v].z, raw.w[v].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -203,11 +202,11 @@ HILS_DI unsigned row_values(const RawRow<T, D>& raw, float (&x)[D / 4]) {
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  // the row's four parts
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+}
+// over the row's four threads
+HILS_DI unsigned row_max(unsigned x) {
+  x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return max(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
 // reductions over the 8 threads that share a column (lanes differing in gq)
@@ -241,7 +240,11 @@ struct DigitOps {
   template <typename T>
   static HILS_DI void make_query(const RawRow<T, D>& raw, int gq, int c4, Query& q) {
     float x[D / 4], down = 0.f, up = 0.f;
-    const unsigned top = row_values<T, D>(raw, x);
+    row_values<T, D>(raw, x);
+    unsigned top = 0;  // bits of the largest magnitude, NaN above infinity
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    top = row_max(top);
     if (top != 0u && top < 0x7f800000u) C::row_factor(__uint_as_float(top), down, up);
     if (top >= 0x7f800000u) up = __uint_as_float(0x7fc00000u);  // a row with an infinity or NaN scores NaN
 #pragma unroll
@@ -372,7 +375,11 @@ struct HalfOps {
   template <typename T>
   static HILS_DI void make_query(const RawRow<T, D>& raw, int, int c4, Query& q) {
     float x[D / 4];
-    const unsigned top = row_values<T, D>(raw, x);
+    row_values<T, D>(raw, x);
+    float largest = 0.f;  // (NaN aside: it stays one in half precision)
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) largest = fmaxf(largest, fabsf(x[i]));
+    const unsigned top = row_max(__float_as_uint(largest));
     // the power of two that brings the largest element into [2^14, 2^15); 2^14
     // for a row that is zero or not finite
     unsigned ex = top >> 23;

@@ -82,6 +82,51 @@ struct RopeView {
   const float* sin_t = nullptr;
   int max_pos = 0, rot = 0, interleaved = 0;
 };
+// Overlapped launches (programmatic dependent launch): a kernel that begins with
+// grid_begin() and is launched by launch_overlapped() may be brought onto the
+// device while the one before it on the stream still runs, and waits in
+// grid_begin() until that one has ended and its writes are visible.  Every thread
+// of every CTA calls it before its first access to global memory and before it
+// returns.  The returned 0 is added to the pointers that are read afterwards
+// (behind()), so that no read of theirs can be moved in front of the wait.
+HILS_DI unsigned long long grid_begin() {
+  unsigned long long zero;
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;\n\tmov.u64 %0, 0;" : "=l"(zero)::"memory");
+  return zero;
+}
+template <typename P>
+HILS_DI void behind(unsigned long long zero, P*& p) {
+  p = reinterpret_cast<P*>(reinterpret_cast<unsigned long long>(p) + zero);
+}
+HILS_DI void behind(unsigned long long zero, CacheView& v) {
+  behind(zero, v.k_pool), behind(zero, v.v_pool), behind(zero, v.k_scale), behind(zero, v.v_scale);
+  behind(zero, v.k_tail), behind(zero, v.v_tail);
+}
+HILS_DI void behind(unsigned long long zero, DecView& v) { behind(zero, v.seq_lens), behind(zero, v.pages); }
+HILS_DI void behind(unsigned long long zero, NewRows& v) {
+  behind(zero, v.k), behind(zero, v.v), behind(zero, v.q), behind(zero, v.q_out), behind(zero, v.row_start);
+  behind(zero, v.positions);
+}
+HILS_DI void behind(unsigned long long zero, RopeView& v) { behind(zero, v.cos_t), behind(zero, v.sin_t); }
+// cluster: CTAs of a cluster along x (1: no clusters)
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 cudaError_t launch_cache_append(const Shape& s, const CacheView& cv, const DecView& dv, const NewRows& rows,
                                 const RopeView& rope, cudaStream_t st, const DevCtx& ctx);
 cudaError_t launch_cache_read(const Shape& s, const CacheView& cv, const DecView& dv, void* k_out, void* v_out,

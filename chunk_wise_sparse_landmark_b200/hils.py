@@ -162,11 +162,11 @@ def load() -> ctypes.CDLL:
         lib.hils_build_summaries_paged.argtypes = [C, PG, P, P, P, P, P]
         lib.hils_score_topk_paged.argtypes = [C, P, PG, P, P, P, P, P, ctypes.c_size_t, P]
         lib.hils_attn_decode_paged.argtypes = [C, P, P, P, PG, P, P, P, P, ctypes.c_size_t, P]
-        CA = ctypes.POINTER(Cache)
-        lib.hils_cache_append.argtypes = [C, PG, CA, ctypes.POINTER(Rows), ctypes.POINTER(Rope), P]
-        lib.hils_build_summaries_cache.argtypes = [C, PG, CA, P, ctypes.c_int32, P, P, P, P]
-        lib.hils_attn_decode_cache.argtypes = [C, P, PG, CA, P, P, P, P, ctypes.c_size_t, P]
-        lib.hils_cache_read.argtypes = [C, PG, CA, P, P, ctypes.c_int32, P]
+        # descriptions go by their addresses (_at), the cheapest form of a call
+        lib.hils_cache_append.argtypes = [P, P, P, P, P, P]
+        lib.hils_build_summaries_cache.argtypes = [P, P, P, P, ctypes.c_int32, P, P, P, P]
+        lib.hils_attn_decode_cache.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.hils_cache_read.argtypes = [P, P, P, P, P, ctypes.c_int32, P]
         lib.hils_workspace_bytes.argtypes = [C, ctypes.c_int32, ctypes.c_int32]
         lib.hils_workspace_bytes.restype = ctypes.c_size_t
         lib.hils_sync_status.argtypes = [P]
@@ -292,33 +292,35 @@ def hils_attn_decode_paged(cfg: Config, q, k_pool, v_pool, pg: Paged, idx, s_sel
 
 # ------------------------------------------------ caches of any format ---
 
+_at = ctypes.addressof  # of a description
+
+
 def _dtype(cfg: Config):
     return torch.float32 if cfg.dtype == HILS_F32 else torch.bfloat16
 
 
-def _t(t: torch.Tensor, shape, dtype, device) -> int:
-    """Address of a contiguous tensor that must have this shape, type and device."""
-    assert t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous(), (
-        f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+def _t(t: torch.Tensor, shape, dtype, at: int) -> int:
+    """Address of a contiguous tensor that must have this shape and type, on CUDA device `at` (-1: CPU)."""
+    assert t.size() == shape and t.dtype is dtype and t.get_device() == at and t.is_contiguous(), (
+        f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on device {at}, "
         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, shape, dtype, device):
+def _rows(t: torch.Tensor, shape, dtype, at: int):
     """Address, row stride and head stride of rows [n, heads, d] whose heads are contiguous."""
     row, head, one = t.stride() if t.ndim == 3 else (0, 0, 0)
-    assert one == 1 and t.shape == shape and t.dtype is dtype and t.device == device, (
-        f"expected {dtype} rows {tuple(shape)} with contiguous heads on {device}, "
+    assert one == 1 and t.size() == shape and t.dtype is dtype and t.get_device() == at, (
+        f"expected {dtype} rows {tuple(shape)} with contiguous heads on device {at}, "
         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr(), row, head
 
 
-def _launch(device, fn, *args, stream):
-    """fn(*args, stream) on the tensors' device (its current stream if None)."""
-    at = device.index
+def _launch(at: int, fn, *args, stream):
+    """fn(*args, stream) on CUDA device `at` (its current stream if None)."""
     raw = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() != at:
-        with torch.cuda.device(device):
+        with torch.cuda.device(at):
             st = fn(*args, raw)
     else:
         st = fn(*args, raw)
@@ -332,29 +334,30 @@ def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) 
     fmt = {torch.float32: HILS_KV_NATIVE, torch.bfloat16: HILS_KV_NATIVE, torch.int8: HILS_KV_I8,
            torch.float8_e4m3fn: HILS_KV_E4M3}.get(k_pool.dtype)
     assert fmt is not None and k_pool.ndim == 4, "pools are [num_pages, Hkv, S, d] of float32, bfloat16, int8 or float8_e4m3fn"
-    dev, (pages, hkv, S, d) = k_pool.device, k_pool.shape
-    c = Cache(_t(k_pool, k_pool.shape, k_pool.dtype, dev), _t(v_pool, k_pool.shape, k_pool.dtype, dev), None, None,
+    at, (pages, hkv, S, d) = k_pool.get_device(), k_pool.shape
+    c = Cache(_t(k_pool, k_pool.shape, k_pool.dtype, at), _t(v_pool, k_pool.shape, k_pool.dtype, at), None, None,
               None, None, fmt)
     c.elements = k_pool.dtype
     if fmt != HILS_KV_NATIVE:
         assert k_scale is not None and v_scale is not None and k_tail is not None and v_tail is not None, (
             "an 8-bit cache needs scales and tails")
-        c.k_scale, c.v_scale = (_t(x, (pages, hkv), torch.float32, dev) for x in (k_scale, v_scale))
+        c.k_scale, c.v_scale = (_t(x, (pages, hkv), torch.float32, at) for x in (k_scale, v_scale))
         assert k_tail.dtype in (torch.float32, torch.bfloat16)
         tail = (k_tail.shape[0], 2, hkv, S, d)
-        c.k_tail, c.v_tail = (_t(x, tail, k_tail.dtype, dev) for x in (k_tail, v_tail))
+        c.k_tail, c.v_tail = (_t(x, tail, k_tail.dtype, at) for x in (k_tail, v_tail))
         c.elements = k_tail.dtype
         c.sequences = k_tail.shape[0]
     else:
         assert k_scale is None and v_scale is None and k_tail is None and v_tail is None, (
             "a native cache has no scales and no tails")
         c.sequences = None
-    c.device, c.tile, c.pages = dev, (hkv, S, d), pages
+    c.at, c.tile, c.pages = at, (hkv, S, d), pages
     c.tensors = (k_pool, v_pool, k_scale, v_scale, k_tail, v_tail)
     return c
 
 
 def _cache_fits(cfg: Config, pg: Paged, c: Cache):
+    assert c.at >= 0, "the cache is not on a CUDA device"
     assert c.tile == (cfg.n_kv_heads, cfg.chunk, cfg.head_dim) and c.elements is _dtype(cfg) and (
         pg.num_pages <= c.pages and c.sequences in (None, cfg.batch)), "the cache does not fit the configuration or its page table"
 
@@ -363,9 +366,9 @@ def rope(cos, sin, interleaved: bool = False) -> Rope:
     """Angle tables: float32 cos and sin [max_pos, rot_dim / 2]; pairs (x[i], x[i + rot_dim / 2]),
     or (x[2i], x[2i + 1]) if interleaved."""
     assert cos.ndim == 2 and cos.is_cuda
-    r = Rope(_t(cos, cos.shape, torch.float32, cos.device), _t(sin, cos.shape, torch.float32, cos.device), cos.shape[0],
+    r = Rope(_t(cos, cos.shape, torch.float32, cos.get_device()), _t(sin, cos.shape, torch.float32, cos.get_device()), cos.shape[0],
              2 * cos.shape[1], int(interleaved))
-    r.device = cos.device
+    r.at = cos.get_device()
     r.tensors = (cos, sin)
     return r
 
@@ -382,23 +385,23 @@ def hils_cache_append(cfg: Config, pg: Paged, cache: Cache, k, v, q=None, q_out=
     """Rotate and append: k, v [n, Hkv, d], q and q_out [n, Hq, d] (views with contiguous heads);
     row_start [B + 1] and positions [n] int32."""
     _cache_fits(cfg, pg, cache)
-    dev, el, n, d = cache.device, cache.elements, k.shape[0], cfg.head_dim
+    at, el, n, d = cache.at, cache.elements, k.shape[0], cfg.head_dim
     shape = (n, cfg.n_kv_heads, d)
-    k, k_row, k_head = _rows(k, shape, el, dev)
-    v, v_row, v_head = _rows(v, shape, el, dev)
+    k, k_row, k_head = _rows(k, shape, el, at)
+    v, v_row, v_head = _rows(v, shape, el, at)
     qa = q_row = q_head = oa = o_row = o_head = 0
     if q is not None:
         assert q_out is not None, "q needs q_out"
         shape = (n, cfg.n_q_heads, d)
-        qa, q_row, q_head = _rows(q, shape, el, dev)
-        oa, o_row, o_head = _rows(q_out, shape, el, dev)
-    start = None if row_start is None else _t(row_start, (cfg.batch + 1,), torch.int32, dev)
-    pos = None if positions is None else _t(positions, (n,), torch.int32, dev)
+        qa, q_row, q_head = _rows(q, shape, el, at)
+        oa, o_row, o_head = _rows(q_out, shape, el, at)
+    start = None if row_start is None else _t(row_start, (cfg.batch + 1,), torch.int32, at)
+    pos = None if positions is None else _t(positions, (n,), torch.int32, at)
     r = Rows(k, v, qa, oa, k_row, k_head, v_row, v_head, q_row, q_head, o_row, o_head, start, pos, n)
     if rope is not None:
-        assert rope.device == dev, "the angle tables are on another device than the cache"
-        rope = ctypes.byref(rope)
-    _launch(dev, load().hils_cache_append, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache), ctypes.byref(r),
+        assert rope.at == at, "the angle tables are on another device than the cache"
+        rope = _at(rope)
+    _launch(at, load().hils_cache_append, _at(cfg), _at(pg), _at(cache), _at(r),
             rope, stream=stream)
 
 
@@ -406,28 +409,28 @@ def hils_build_summaries_cache(cfg: Config, pg: Paged, cache: Cache, q_lmk, k_su
     """Summaries over a cache of any format; q_lmk [B, Hq, C, d], one for each sequence
     [B, Hq, d], or one for all [Hq, d]; from_lens [B] int32: only chunks completed since."""
     _cache_fits(cfg, pg, cache)
-    dev, B, hq, d = cache.device, cfg.batch, cfg.n_q_heads, cfg.head_dim
+    at, B, hq, d = cache.at, cfg.batch, cfg.n_q_heads, cfg.head_dim
     C = cfg.seq_len // cfg.chunk
     lmk, shape = {4: (HILS_LMK_CHUNK, (B, hq, C, d)), 3: (HILS_LMK_SEQUENCE, (B, hq, d)),
                   2: (HILS_LMK_SHARED, (hq, d))}[q_lmk.ndim]
     el = cache.elements
-    _launch(dev, load().hils_build_summaries_cache, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache),
-            _t(q_lmk, shape, el, dev), lmk, None if from_lens is None else _t(from_lens, (B,), torch.int32, dev),
-            _t(k_sum, (B, hq, C, d), el, dev), _t(b_sum, (B, hq, C), torch.float32, dev), stream=stream)
+    _launch(at, load().hils_build_summaries_cache, _at(cfg), _at(pg), _at(cache),
+            _t(q_lmk, shape, el, at), lmk, None if from_lens is None else _t(from_lens, (B,), torch.int32, at),
+            _t(k_sum, (B, hq, C, d), el, at), _t(b_sum, (B, hq, C), torch.float32, at), stream=stream)
 
 
 def hils_attn_decode_cache(cfg: Config, q, pg: Paged, cache: Cache, idx, s_sel, out, workspace=None, stream=None):
     """Decode attention over a cache of any format (workspace: native caches only)."""
     _cache_fits(cfg, pg, cache)
-    dev, B, hq, K, el = cache.device, cfg.batch, cfg.n_q_heads, cfg.top_k, cache.elements
+    at, B, hq, K, el = cache.at, cfg.batch, cfg.n_q_heads, cfg.top_k, cache.elements
     ws, ws_bytes = None, 0
     if workspace is not None:
-        assert workspace.device == dev and workspace.is_contiguous()
+        assert workspace.get_device() == at and workspace.is_contiguous()
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     row = (B, hq, cfg.head_dim)
-    _launch(dev, load().hils_attn_decode_cache, ctypes.byref(cfg), _t(q, row, el, dev), ctypes.byref(pg),
-            ctypes.byref(cache), _t(idx, (B, cfg.n_kv_heads, K), torch.int32, dev),
-            _t(s_sel, (B, hq, K), torch.float32, dev), _t(out, row, el, dev), ws, ws_bytes, stream=stream)
+    _launch(at, load().hils_attn_decode_cache, _at(cfg), _t(q, row, el, at), _at(pg),
+            _at(cache), _t(idx, (B, cfg.n_kv_heads, K), torch.int32, at),
+            _t(s_sel, (B, hq, K), torch.float32, at), _t(out, row, el, at), ws, ws_bytes, stream=stream)
 
 
 def hils_cache_read(cfg: Config, pg: Paged, cache: Cache, k_out=None, v_out=None, stream=None):
@@ -436,8 +439,8 @@ def hils_cache_read(cfg: Config, pg: Paged, cache: Cache, k_out=None, v_out=None
     some = k_out if k_out is not None else v_out
     assert some is not None and some.ndim == 4, "k_out or v_out [B, Hkv, rows, d] is needed"
     shape = (cfg.batch, cfg.n_kv_heads, some.shape[2], cfg.head_dim)
-    k, v = (None if t is None else _t(t, shape, cache.elements, cache.device) for t in (k_out, v_out))
-    _launch(cache.device, load().hils_cache_read, ctypes.byref(cfg), ctypes.byref(pg), ctypes.byref(cache), k, v,
+    k, v = (None if t is None else _t(t, shape, cache.elements, cache.at) for t in (k_out, v_out))
+    _launch(cache.at, load().hils_cache_read, _at(cfg), _at(pg), _at(cache), k, v,
             some.shape[2], stream=stream)
 
 
