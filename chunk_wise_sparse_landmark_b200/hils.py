@@ -89,6 +89,7 @@ class Paged(ctypes.Structure):
         ("max_pages", ctypes.c_int32),
         ("num_pages", ctypes.c_int32),
     ]
+    batch = None  # sequences of the tables, where known (paged())
 
 
 class Cache(ctypes.Structure):
@@ -265,6 +266,7 @@ def paged(seq_lens, block_table, num_pages: int) -> Paged:
     assert seq_lens.dtype == torch.int32 and block_table.dtype == torch.int32
     pg = Paged(_p(seq_lens).value, _p(block_table).value, block_table.shape[1], num_pages)
     pg.tensors = (seq_lens, block_table)  # the description keeps what it points to
+    pg.batch = min(seq_lens.shape[0], block_table.shape[0])
     return pg
 
 
@@ -359,7 +361,7 @@ def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) 
 def _cache_fits(cfg: Config, pg: Paged, c: Cache):
     assert c.at >= 0, "the cache is not on a CUDA device"
     assert c.tile == (cfg.n_kv_heads, cfg.chunk, cfg.head_dim) and c.elements is _dtype(cfg) and (
-        pg.num_pages <= c.pages and c.sequences in (None, cfg.batch)), "the cache does not fit the configuration or its page table"
+        pg.num_pages <= c.pages and c.sequences in (None, cfg.batch) and pg.batch in (None, cfg.batch)), "the cache does not fit the configuration or its page table"
 
 
 def rope(cos, sin, interleaved: bool = False) -> Rope:
@@ -593,7 +595,7 @@ class CacheDecode:
         self.idx = torch.empty((B, Hkv, K), dtype=torch.int32, device=dev)
         self.s_sel = torch.empty((B, Hq, K), dtype=torch.float32, device=dev)
         self.out = torch.empty((B, Hq, d), dtype=dt, device=dev)
-        self.ws_score = alloc_workspace(workspace_bytes(cfg, HILS_WS_SCORE_DECODE), dev)
+        self.ws_score = alloc_workspace(max(16, workspace_bytes(cfg, HILS_WS_SCORE_DECODE)), dev)
         self.ws_attn = None if rest else alloc_workspace(workspace_bytes(cfg, HILS_WS_ATTN_DECODE), dev)
 
     def append(self, k, v, q_lmk, q=None, q_out=None, row_start=None, from_lens=None, positions=None, stream=None):

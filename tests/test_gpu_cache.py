@@ -328,6 +328,32 @@ def test_one_row_for_each_sequence_without_row_start_and_no_rows():
     c.check()
 
 
+def test_one_row_each_of_more_sequences_than_a_chunk_has_tokens():
+    c = Case(150, 2, 1, 64, 32, 70, F32, E4)
+    rng = np.random.default_rng(4)
+    old = rng.integers(0, 69, 150).tolist()
+    c.fill(old)
+    angles, rope = c.rope(64, False)
+    k, v, q = c.rand(150, 1, 64), c.rand(150, 1, 64), c.rand(150, 2, 64)
+    lens = [L + 1 for L in old]
+    q_out = torch.empty_like(q, device=DEV)
+    H.hils_cache_append(c.cfg, c.paged(lens), c.cache, k.to(DEV), v.to(DEV), q.to(DEV), q_out, rope)
+    a = (angles[0][torch.tensor(old)], angles[1][torch.tensor(old)])
+    c.ref.append(lens, [1] * 150, rotate(k, *a, False), v)
+    c.check()
+    assert same(q_out, rotate(q, *a, False))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (7, 7), (96, 12), (160, 20)])
+@pytest.mark.parametrize("n", [3, 2100])
+def test_any_number_of_heads(Hq, Hkv, n):
+    """Fewer heads than a row has lanes, odd numbers, and more than one pass over the heads."""
+    c = Case(1, Hq, Hkv, 128, 64, 2112, BF, I8)
+    angles, rope = c.rope(64, True)
+    c.append([n], [n], c.rand(n, Hkv, 128), c.rand(n, Hkv, 128), c.rand(n, Hq, 128), rope, angles, True)
+    c.check()
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads."""
     B = 700
@@ -558,6 +584,59 @@ def test_attention_list_lengths_and_windows(code, K, W):
     H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), out)
     H.hils_sync_status()
     c.check_attention(lens, q, idx, s_sel, out)
+
+
+@pytest.mark.parametrize("B", [2, 20, 45, 90, 300, 520, 1000, 1900])
+@pytest.mark.parametrize("dtype,d,S,code,G", [(BF, 128, 64, I8, 2), (BF, 128, 64, E4, 4), (F32, 64, 32, I8, 1)],
+                         ids=["bf16-i8", "bf16-e4m3", "f32-i8"])
+def test_attention_and_summaries_of_any_number_of_sequences(B, dtype, d, S, code, G):
+    """One launch shape after the other: clusters of CTAs, one CTA of 12 to 3 warps, several waves of four; summaries
+    over more sequences than one block of CTAs takes."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, 5 * S, B).tolist()
+    c = Case(B, G, 1, d, S, 5 * S, dtype, code, W=2 * S, K=3)
+    c.fill(lens)
+    q, ql = c.rand(B, G, d), c.rand(B, G, 5, d)
+    idx, s_sel = c.lists(lens)
+    out = torch.full((B, G, d), math.nan, dtype=dtype, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    ks, bs = torch.full((B, G, 5, d), 3.0, dtype=dtype), torch.full((B, G, 5), 4.0)
+    k_sum, b_sum = ks.to(DEV), bs.to(DEV)
+    H.hils_build_summaries_cache(c.cfg, c.paged(lens), c.cache, ql.to(DEV), k_sum, b_sum)
+    H.hils_sync_status()
+    some = sorted({0, 1, B // 3, B // 2, B - 2, B - 1} | set(rng.integers(0, B, 12).tolist()))
+    for b in some:
+        k, v = c.ref.values(0, b, lens[b]), c.ref.values(1, b, lens[b])
+        want, mag, low, big, wide = attend(q[b].double(), k, v, idx[b].tolist(), s_sel[b].double(), S, c.W, c.scale)
+        rel = weights_off(dtype, code, d, S, 3 * S + c.W, big, wide)
+        assert out_off(dtype, out[b], want, mag, low, rel) <= 0, (b, lens[b])
+    assert out.isfinite().all()
+    check_summaries(c, lens, [0] * B, lambda b, ch: ql[b][:, list(ch)].double(), k_sum, b_sum, ks, bs)
+
+
+@pytest.mark.parametrize("code", [I8, E4], ids=["i8", "e4m3"])
+def test_attention_with_more_units_than_a_warp_looks_ahead(code):
+    """512 sequences of 64 chosen chunks and a window of 32: three warps each, 32 units a warp."""
+    B, L = 512, 100 * 64 - 5
+    c = Case(1, 2, 1, 128, 64, 100 * 64, BF, code, W=32 * 64, K=64)
+    c.fill([L])
+    idx, s_sel = c.lists([L])
+    q = c.rand(B, 2, 128)
+    cfg = H.make_config(B, 100 * 64, 2, 1, 128, 64, 32 * 64, 64, BF)
+    # every sequence reads the same pages and the same tail rows
+    tails = [t.expand(B, *t.shape[1:]).contiguous() for t in c.dev[2]]
+    cache = H.cache(*c.dev[0], *c.dev[1], *tails)
+    table = c.table_dev.expand(B, -1).contiguous()
+    pg = H.paged(torch.full((B,), L, dtype=torch.int32, device=DEV), table, c.pages)
+    out = torch.empty((B, 2, 128), dtype=BF, device=DEV)
+    H.hils_attn_decode_cache(cfg, q.to(DEV), pg, cache, idx.expand(B, -1, -1).contiguous().to(DEV),
+                             s_sel.expand(B, -1, -1).contiguous().to(DEV), out)
+    H.hils_sync_status()
+    k, v = c.ref.values(0, 0, L), c.ref.values(1, 0, L)
+    for b in (0, 1, 255, 511):
+        want, mag, low, big, wide = attend(q[b].double(), k, v, idx[0].tolist(), s_sel[0].double(), 64, c.W, c.scale)
+        rel = weights_off(BF, code, 128, 64, 96 * 64, big, wide)
+        assert out_off(BF, out[b], want, mag, low, rel) <= 0, b
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
