@@ -81,8 +81,7 @@ __global__ void __launch_bounds__(kThreads) native_summaries_kernel(Shape s, Cac
 // ---------------------------------------------------------------------------
 // 8-bit caches: warps work on their own, each on one tile of codes at a time
 // (code_mma.cuh), which lane 0 fetches by TMA into the warp's two buffers.
-constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 3;  // 16 KB of buffers a warp at d = 128, S = 64
+constexpr int kWarps = 4;  // of a CTA that builds summaries
 
 template <int D, int S>
 struct alignas(1024) WarpBuffers {
@@ -91,7 +90,7 @@ struct alignas(1024) WarpBuffers {
 // the buffers' start: a multiple of 1024 bytes, as the swizzle counts lines
 HILS_DI unsigned char* align_1k(unsigned char* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
 template <int D, int S>
-constexpr size_t buffer_bytes() { return sizeof(WarpBuffers<D, S>) * kWarps + 1024; }
+HILS_DI Tile<D, S> tile_of(const uint8_t* p) { return Tile<D, S>{{p, p + S * D / 2}}; }
 template <int D, int S>
 HILS_DI void fetch_tile(void* dst, const CUtensorMap* map, int tile, uint64_t* bar, const DevCtx& ctx) {
   if (ctx.inject == 1) return;  // test hook: no copy, the wait must run out
@@ -162,28 +161,38 @@ HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = 
 // Warps take the chunks of all sequences in turn, so that short and long
 // sequences share the work evenly.  A CTA serves sequences [kSeqs blockIdx.y, +
 // kSeqs): their numbers of chunks are summed up in shared memory, and unit u is
-// KV head u % Hkv of chunk u / Hkv of that order.  Two buffers for the tiles; the
-// landmark rows of the next unit are asked for before this one is computed.
+// KV head u % Hkv of chunk u / Hkv of that order.  Computing bounds it (about 1000
+// instructions of a warp for a tile of 8 KB), so that many warps matter: a warp
+// has three half tiles of buffer, 12 KB, and sixteen warps share a
+// multiprocessor.  It holds a tile and the first half of the next one, whose
+// second half takes the place of this one's first half once that has been read.
+// The landmark rows of the next unit are asked for before this one is computed.
 constexpr int kSeqs = 512;
+template <typename T>
+constexpr int summary_ctas() { return sizeof(T) == 2 ? 4 : 3; }  // of a multiprocessor
+template <int D, int S>
+struct alignas(1024) HalfTiles {
+  uint8_t h[3][S * D / 2];
+};
 
 template <typename T, typename C, int D, int S, int G>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel(
+__global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries_kernel(
     const __grid_constant__ CUtensorMap kmap, Shape s, CacheView cv, DecView dv, const T* q_lmk,
     LmkStrides ls, const int* from, T* k_sum, float* b_sum, DevCtx ctx) {
   using Ops = typename OpsOf<T, C, D, S, G>::type;
   constexpr int R = Ops::R, N8 = D / 8;
   constexpr int PER = kSeqs / (kWarps * 32);  // sequences of a thread
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t bars[kWarps][2];
+  __shared__ uint64_t bars[kWarps][3];
   __shared__ int ends[kSeqs], firsts[kSeqs], sums[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, c4 = lane & 3;
   const int b0 = blockIdx.y * kSeqs, nb = min(kSeqs, s.B - b0);
-  WarpBuffers<D, S>& buf = reinterpret_cast<WarpBuffers<D, S>*>(align_1k(smem_raw))[warp];
+  HalfTiles<D, S>& buf = reinterpret_cast<HalfTiles<D, S>*>(align_1k(smem_raw))[warp];
   uint64_t* bar = bars[warp];
   if (lane == 0) {
     prefetch_tmap(&kmap);
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) mbar_init(&bar[x], 1);
     fence_barrier_init();
     fence_proxy_async_shared();
   }
@@ -269,35 +278,48 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
   auto ask_query = [&](const Unit& x, RawRow<T, D>& raw) {
     raw.load(row < G ? q_lmk + ls.of(x.b, x.g * G + row, x.c) : (const T*)nullptr, c4);
   };
+  // Half tiles n = 0, 1, 2 .. (two to a unit) go to buffers n % 3.  A unit whose
+  // page is outside the pool is fetched as tile 0 and left out.
+  int n_asked = 0;  // half tiles asked for
+  auto ask_half = [&](int tile) {
+    const int slot = n_asked % 3, half = n_asked & 1;
+    if (lane == 0 && ctx.inject != 1) {  // (test hook: no copy, the wait must run out)
+      mbar_arrive_expect_tx(&bar[slot], S * D / 2);
+      tma_load_2d(buf.h[slot], &kmap, 0, max(tile, 0) * (S * D / 128) + half * (S * D / 256), &bar[slot]);
+    }
+    ++n_asked;
+  };
   look_up(u);
-  Unit now = unit_of(0);
+  Unit now = unit_of(0), next;
+  ask_half(now.tile);
+  ask_half(now.tile);
   RawRow<T, D> raw;
-  if (now.tile >= 0) {
-    if (lane == 0) fetch_tile<D, S>(buf.a, &kmap, now.tile, &bar[0], ctx);
-    ask_query(now, raw);
+  ask_query(now, raw);
+  next.tile = -1;
+  if (u + step < units) {
+    next = unit_of(1);
+    ask_half(next.tile);
   }
-  bool flying[2] = {now.tile >= 0, false};
-  uint32_t phase[2] = {0u, 0u};
   bool alive = true;
-  for (int i = 0; u < units; u += step, ++i) {
-    const int st = i & 1;
-    Unit next;
-    next.tile = -1;
-    if (u + step < units) {
-      if (((i + 1) & 31) == 0) look_up(u + step);
-      next = unit_of(i + 1);
-      if (lane == 0 && next.tile >= 0) fetch_tile<D, S>(st ? buf.a : buf.b, &kmap, next.tile, &bar[st ^ 1], ctx);
-      flying[st ^ 1] = next.tile >= 0;
+  int i = 0;
+  for (; u < units; u += step, ++i) {
+    const bool more = u + step < units;
+    // behind the next unit: its first half follows this unit's second half
+    Unit later;
+    later.tile = -1;
+    const bool more2 = u + 2 * step < units;
+    if (more2) {
+      if (((i + 2) & 31) == 0) look_up(u + 2 * step);
+      later = unit_of(i + 2);
     }
     typename Ops::Query q;
-    if (now.tile >= 0) Ops::template make_query<T>(raw, gq, c4, q);
-    if (next.tile >= 0) ask_query(next, raw);
-    if (now.tile >= 0) {
-      alive = mbar_wait(&bar[st], phase[st], ctx);
-      if (!__all_sync(0xffffffffu, alive)) break;
-      phase[st] ^= 1u;
-      flying[st] = false;
-      const uint8_t* t = st ? buf.b : buf.a;
+    Ops::template make_query<T>(raw, gq, c4, q);
+    if (more) ask_query(next, raw);
+    const int n0 = 2 * i, s0 = n0 % 3, s1 = (n0 + 1) % 3;
+    alive = mbar_wait(&bar[s0], (n0 / 3) & 1, ctx) && mbar_wait(&bar[s1], ((n0 + 1) / 3) & 1, ctx);
+    if (!__all_sync(0xffffffffu, alive)) break;
+    {
+      const Tile<D, S> t{{buf.h[s0], buf.h[s1]}};
       float sc[R][S / 8], o[R][N8], inv[R];
       Ops::scores(t, at, q, sc);
       const long long h0 = (long long)now.b * s.Hq + now.g * G;
@@ -307,13 +329,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
         float top, z, zl;
         weigh<Ops>(sc[r], s.scale * now.ks * q.up[r], top, z, &zl);
         inv[r] = __fdividef(now.ks, z);
-        if (h < G && gq == 0) b_sum[(h0 + h) * s.C + now.c] = logf(z * (1.f / Ops::kOne)) - __fdividef(zl, z);
+        if (h < G && gq == 0 && now.tile >= 0) b_sum[(h0 + h) * s.C + now.c] = logf(z * (1.f / Ops::kOne)) - __fdividef(zl, z);
       }
-      Ops::values(t, at, gq, sc, o);
+      Ops::values(t, at, gq, sc, o, [&] {
+        __syncwarp();  // every lane has read the first half
+        if (more) ask_half(next.tile);
+      });
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = Ops::head(r, c4);
-        if (h >= G) continue;
+        if (h >= G || now.tile < 0) continue;
         T* dst = k_sum + ((h0 + h) * s.C + now.c) * D + gq * N8;
 #pragma unroll
         for (int x = 0; x < N8; ++x) o[r][x] *= inv[r];
@@ -330,12 +355,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) code_summaries_kernel
         }
       }
     }
-    __syncwarp();  // every lane has read the buffer that the next round refills
+    __syncwarp();  // every lane has read the second half
+    if (more2) ask_half(later.tile);
     now = next;
+    next = later;
   }
-  if (!__all_sync(0xffffffffu, alive) && lane == 0)  // let the copies in flight land before the buffers go
-    for (int st = 0; st < 2; ++st)
-      if (flying[st] && ctx.inject != 1) mbar_wait(&bar[st], phase[st], ctx);
+  if (!__all_sync(0xffffffffu, alive) && lane == 0 && ctx.inject != 1)  // let the copies in flight land first
+    for (int n = 2 * i; n < n_asked; ++n) mbar_wait(&bar[n % 3], (n / 3) & 1, ctx);
 }
 
 // ------------------------------------------------------------ cluster access ---
@@ -661,7 +687,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     if (!__all_sync(0xffffffffu, alive)) break;
     flying[0] = false;
     phase[0] ^= 1u;
-    Ops::scores(buf.a, at, qr, sc);
+    Ops::scores(tile_of<D, S>(buf.a), at, qr, sc);
     __syncwarp();  // every lane has read the keys: their buffer takes the next unit's
     if (next >= 0) {
       if (lane == 0) fetch_tile<D, S>(buf.a, &kmap, next, &bar[0], ctx);
@@ -681,7 +707,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     if (!__all_sync(0xffffffffu, alive)) break;
     flying[1] = false;
     phase[1] ^= 1u;
-    Ops::values(buf.b, at, gq, sc, o);
+    Ops::values(tile_of<D, S>(buf.b), at, gq, sc, o, [] {});
     __syncwarp();
     if (next >= 0) {
       if (lane == 0) fetch_tile<D, S>(buf.b, &vmap, next, &bar[1], ctx);
@@ -766,17 +792,17 @@ template <typename T, typename C, int D, int S, int G>
 cudaError_t go_summ(const Shape& s, const CacheView& cv, const DecView& dv, const void* q_lmk, const LmkStrides& ls,
                     const int* from, void* k_sum, float* b_sum, cudaStream_t st, const DevCtx& ctx) {
   if (s.C == 0) return cudaSuccess;
-  const size_t smem = buffer_bytes<D, S>();
+  const size_t smem = sizeof(HalfTiles<D, S>) * kWarps + 1024;
   auto kern = code_summaries_kernel<T, C, D, S, G>;
   cudaError_t e = ensure_dynamic_smem((const void*)kern, (int)smem);
   if (e != cudaSuccess) return e;
   CUtensorMap km;
-  e = make_tmap_rows128(&km, cv.k_pool, (uint64_t)dv.num_pages * s.Hkv * (S * D / 128), S * D / 128);
+  e = make_tmap_rows128(&km, cv.k_pool, (uint64_t)dv.num_pages * s.Hkv * (S * D / 128), S * D / 256);
   if (e != cudaSuccess) return e;
   // one wave of CTAs, fewer if there are not as many chunks
   const int blocks = (s.B + kSeqs - 1) / kSeqs;
   const long long most = ((long long)(s.B < kSeqs ? s.B : kSeqs) * s.C * s.Hkv + kWarps - 1) / kWarps;
-  const long long wave = (device_sm_count() * kCtasPerSm + blocks - 1) / blocks;
+  const long long wave = (device_sm_count() * summary_ctas<T>() + blocks - 1) / blocks;
   return launch_overlapped(kern, dim3((unsigned)(wave < most ? wave : most), blocks), kWarps * 32, smem, 1, st, km, s, cv,
                            dv, (const T*)q_lmk, ls, from, (T*)k_sum, b_sum, ctx);
 }

@@ -34,7 +34,8 @@
 //   the D / 4 dims from c4 D / 4 on, in words of four codes.  The eight lanes of
 //   one of a load's phases touch all eight pieces of a line once.  Result
 //   sc[r][2 mt + hi]: key 16 mt + gq + 8 hi, head head(r, c4).
-// * values: a thread holds dims gq D / 8 + x, x < D / 8: result o[r][x].
+// * values: a thread holds dims gq D / 8 + x, x < D / 8: result o[r][x]; half_read()
+//   is called once what the thread read of the tile's first half has been used.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -94,6 +95,17 @@ HILS_DI float exp_neg(float x) { return exp2_fast(x * kLog2e); }
 
 // byte offset of linear byte `o` of a tile
 HILS_DI int swz(int o) { return o ^ (((o >> 7) & 7) << 4); }
+// A tile in two halves of S / 2 keys.
+template <int D, int S>
+struct Tile {
+  const uint8_t* h[2];
+  // the 16 keys of m-tile mt
+  HILS_DI const uint8_t* keys16(int mt) const {
+    constexpr int M = S / 32;
+    return (mt < M ? h[0] : h[1]) + 16 * (mt < M ? mt : mt - M) * D;
+  }
+};
+
 // Offsets of a thread's parts in a tile; the pattern repeats every 16 keys.
 template <int D>
 struct TileOffsets {
@@ -257,7 +269,7 @@ struct DigitOps {
     }
     q.up[0] = __shfl_sync(0xffffffffu, up, 8 * c4);
   }
-  static HILS_DI void scores(const uint8_t* t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
+  static HILS_DI void scores(const Tile<D, S>& t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
     constexpr int V = D / 64;
 #pragma unroll
     for (int mt = 0; mt < S / 16; ++mt) {
@@ -266,7 +278,7 @@ struct DigitOps {
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
-          const uint4 x = *reinterpret_cast<const uint4*>(t + at.k[v][hi] + 16 * mt * D);
+          const uint4 x = *reinterpret_cast<const uint4*>(t.keys16(mt) + at.k[v][hi]);
           w[hi][4 * v] = x.x, w[hi][4 * v + 1] = x.y, w[hi][4 * v + 2] = x.z, w[hi][4 * v + 3] = x.w;
         }
 #pragma unroll
@@ -286,8 +298,9 @@ struct DigitOps {
       }
     }
   }
-  static HILS_DI void values(const uint8_t* t, const TileOffsets<D>& at, int gq, const float (&p)[R][S / 8],
-                             float (&o)[R][D / 8]) {
+  template <typename F>
+  static HILS_DI void values(const Tile<D, S>& t, const TileOffsets<D>& at, int gq, const float (&p)[R][S / 8],
+                             float (&o)[R][D / 8], F half_read) {
     // P^T fragments.  A 16-bit element holds the two digits of a weight; the
     // transpose leaves a thread (gq, c4) with head gq / 2 of keys 2 c4 and 2 c4 + 1
     // (+ 8 if gq is odd); it keeps the digit of its column and gets its
@@ -316,7 +329,7 @@ struct DigitOps {
       for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint8_t* a = t + at.v[e] + 16 * (2 * kk + half) * D;
+          const uint8_t* a = t.keys16(2 * kk + half) + at.v[e];
           if (W == 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(a);
             w[half][e][0] = x.x, w[half][e][1] = x.y, w[half][e][W - 2] = x.z, w[half][e][W - 1] = x.w;
@@ -350,6 +363,7 @@ struct DigitOps {
           }
         }
       }
+      if (2 * kk + 2 == S / 32) half_read();
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -399,15 +413,15 @@ struct HalfOps {
 #pragma unroll
     for (int r = 0; r < R; ++r) q.up[r] = __shfl_sync(0xffffffffu, up, 4 * (2 * c4 + r));
   }
-  static HILS_DI void scores(const uint8_t* t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
+  static HILS_DI void scores(const Tile<D, S>& t, const TileOffsets<D>& at, const Query& q, float (&sc)[R][S / 8]) {
     constexpr int V = D / 64;
 #pragma unroll
     for (int mt = 0; mt < S / 16; ++mt) {
       float d[4];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const uint4 a = *reinterpret_cast<const uint4*>(t + at.k[v][0] + 16 * mt * D),
-                    b = *reinterpret_cast<const uint4*>(t + at.k[v][1] + 16 * mt * D);
+        const uint4 a = *reinterpret_cast<const uint4*>(t.keys16(mt) + at.k[v][0]),
+                    b = *reinterpret_cast<const uint4*>(t.keys16(mt) + at.k[v][1]);
         const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -426,8 +440,9 @@ struct HalfOps {
       for (int r = 0; r < R; ++r) sc[r][2 * mt] = d[r], sc[r][2 * mt + 1] = d[2 + r];
     }
   }
-  static HILS_DI void values(const uint8_t* t, const TileOffsets<D>& at, int, const float (&p)[R][S / 8],
-                             float (&o)[R][D / 8]) {
+  template <typename F>
+  static HILS_DI void values(const Tile<D, S>& t, const TileOffsets<D>& at, int, const float (&p)[R][S / 8],
+                             float (&o)[R][D / 8], F half_read) {
     constexpr int W = D / 32;  // words of a thread's part of a key
     float d[D / 16][4];
 #pragma unroll
@@ -443,7 +458,7 @@ struct HalfOps {
       uint32_t w[4][W];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint8_t* a = t + at.v[e] + 16 * kk * D;
+        const uint8_t* a = t.keys16(kk) + at.v[e];
         if (W == 4) {
           const uint4 x = *reinterpret_cast<const uint4*>(a);
           w[e][0] = x.x, w[e][1] = x.y, w[e][W - 2] = x.z, w[e][W - 1] = x.w;
@@ -470,6 +485,7 @@ struct HalfOps {
           else mma_f16_16816(d[2 * j + 1], A, b0[q], b1[q]);
         }
       }
+      if (kk + 1 == S / 32) half_read();
     }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
