@@ -369,11 +369,22 @@ HILS_DI void cluster_sync() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-HILS_DI float peer_f32(const float* p, int rank) {
+HILS_DI uint32_t peer_addr(const float* p, int rank) {
   uint32_t a;
-  float x;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return a;
+}
+HILS_DI float peer_f32(const float* p, int rank) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(peer_addr(p, rank)) : "memory");
+  return x;
+}
+HILS_DI float4 peer_f32x4(const float* p, int rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
   return x;
 }
 // A running maximum starts at -inf and is compared as no less than kLeast, so
@@ -513,6 +524,7 @@ struct TailSlice<__nv_bfloat16, Ops, D> {
 };
 
 constexpr int kMaxUnits = 64 + 32;  // K list entries, W / S window chunks
+constexpr int kMaxCtas = 8;         // of a cluster
 constexpr int kMaxWarps = 12;       // 16 KB of buffers each at d = 128, S = 64, up to 170 registers a thread
 
 // A cluster of CTAs serves one (sequence, KV head).  Units, dealt to the
@@ -751,20 +763,33 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   }
   __syncthreads();
   T* o0 = out + ((long long)b * s.Hq + g * G) * D;
-  for (int x = threadIdx.x; x < G * D; x += blockDim.x) {
+  // four dims of a head at a time
+  auto add = [](float4& n, float f, const float4& x) {
+    n.x = fmaf(f, x.x, n.x), n.y = fmaf(f, x.y, n.y), n.z = fmaf(f, x.z, n.z), n.w = fmaf(f, x.w, n.w);
+  };
+  auto write = [&](int x, const float4& n, float d) {
+    const float4 y = make_float4(n.x / d, n.y / d, n.z / d, n.w / d);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(o0 + x) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    else
+      *reinterpret_cast<float4*>(o0 + x) = y;
+  };
+  for (int x = 4 * threadIdx.x; x < G * D; x += 4 * blockDim.x) {
     const int h = x / D;
-    float Mx = kLeast;
+    float Mx = kLeast, dd = 0.f;
+#pragma unroll 4
     for (int w = 0; w < nwarp; ++w) Mx = fmaxf(Mx, red_m[w][h]);
-    float num = 0.f, dd = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int w = 0; w < nwarp; ++w) {
       const float f = exp_neg(red_m[w][h] - Mx);
-      num += f * rec[w * G * D + x];
-      dd += f * red_d[w][h];
+      add(num, f, *reinterpret_cast<const float4*>(rec + w * G * D + x));
+      dd = fmaf(f, red_d[w][h], dd);
     }
     if (ncta == 1) {
-      o0[x] = from_f32<T>(num / dd);
+      write(x, num, dd);
     } else {
-      cta[x] = num;
+      *reinterpret_cast<float4*>(cta + x) = num;
       if (x % D == 0) {
         cta_m[h] = Mx;
         cta_d[h] = dd;
@@ -773,17 +798,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   }
   if (ncta == 1) return;
   cluster_sync();
-  for (int x = rank * blockDim.x + threadIdx.x; x < G * D; x += ncta * blockDim.x) {
+  for (int x = 4 * (rank * blockDim.x + threadIdx.x); x < G * D; x += 4 * ncta * blockDim.x) {
     const int h = x / D;
-    float Mx = kLeast;
-    for (int w = 0; w < ncta; ++w) Mx = fmaxf(Mx, peer_f32(&cta_m[h], w));
-    float num = 0.f, dd = 0.f;
-    for (int w = 0; w < ncta; ++w) {
-      const float f = exp_neg(peer_f32(&cta_m[h], w) - Mx);
-      num += f * peer_f32(cta + x, w);
-      dd += f * peer_f32(&cta_d[h], w);
+    // all of the other CTAs' records at once
+    float m[kMaxCtas], d[kMaxCtas], Mx = kLeast, dd = 0.f;
+    float4 n[kMaxCtas], num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kMaxCtas; ++w) {
+      const int from = w < ncta ? w : 0;
+      m[w] = peer_f32(&cta_m[h], from);
+      d[w] = peer_f32(&cta_d[h], from);
+      n[w] = peer_f32x4(cta + x, from);
     }
-    o0[x] = from_f32<T>(num / dd);
+#pragma unroll
+    for (int w = 0; w < kMaxCtas; ++w) Mx = w < ncta ? fmaxf(Mx, m[w]) : Mx;
+#pragma unroll
+    for (int w = 0; w < kMaxCtas; ++w) {
+      if (w >= ncta) continue;
+      const float f = exp_neg(m[w] - Mx);
+      add(num, f, n[w]);
+      dd = fmaf(f, d[w], dd);
+    }
+    write(x, num, dd);
   }
   cluster_sync();  // no CTA leaves while its records are read
 }
@@ -841,7 +877,7 @@ cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const De
   // each, down to one unit a warp.
   const int sms = device_sm_count(), groups = s.B * s.Hkv, units = s.K + s.nw + 3;
   int ncta = sms / groups;
-  ncta = ncta < 1 ? 1 : ncta > 8 ? 8 : ncta;
+  ncta = ncta < 1 ? 1 : ncta > kMaxCtas ? kMaxCtas : ncta;
   int share = sms * kMaxWarps / groups;
   share = share < 3 ? 4 : share;
   share = share < units ? share : units;
