@@ -15,7 +15,10 @@
 // rows of a chunk that completes from the tail, everything in registers between
 // load and store.  The other rotates rows of the queries.  Both read each element
 // once and write it once.  Alone, the first is bound by its instructions and
-// waits (scale, then codes), the second by the memory, so they are mixed.
+// waits (scale, then codes), the second by the memory, so they are mixed: 32768
+// rows, 32 heads over 8, int8: 141 us, 5.4 TB/s of the 755 MB it must move; the
+// kinds one after the other 156; the first kind alone 70 us (2.9 TB/s).  8192 rows
+// into bf16 pages: 36.1 us, 5.7 TB/s.  48 single float32 rows: 3.6 us.
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -490,7 +493,8 @@ HILS_DI void store16(__nv_bfloat16* p, const float (&x)[16]) {
 }
 
 // One CTA per (chunk, KV head, sequence; keys or values): a tile is contiguous
-// in the pool and in the output.
+// in the pool and in the output.  Bound by memory: 32768 rows, 8 heads, int8 to
+// bf16: 33.6 us, 6.0 TB/s.
 template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView cv, DecView dv, T* __restrict__ k_out,
                                                               T* __restrict__ v_out, int out_rows, DevCtx ctx) {

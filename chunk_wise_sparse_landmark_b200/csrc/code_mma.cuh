@@ -23,10 +23,11 @@
 // The sum of the weights is always taken in float32 from the unrounded ones.
 //
 // Which: widening costs an int8 code five instructions for four codes on the
-// pipe that limits, an e4m3 code two or three.  Decode attention over 64
-// sequences of 16K, K = 32, W = 512, us, DigitOps : HalfOps: int8, G = 1, 4, 8:
-// 63.8 : 68.5, 65.4 : 70.7, 92.4 : 67.7 (eight heads need two blocks of columns);
-// with e4m3 digits 70.6 : 66.0, 72.5 : 71.0, 96.1 : 73.0 (not kept).
+// pipe that limits, an e4m3 code two or three.  DigitOps : HalfOps, us: decode
+// attention over int8, 64 sequences of 16K (K = 32, W = 512), G = 1 56.9 : 60.5,
+// G = 4 58.2 : 62.4; summaries of 55K tokens, G = 2, 18.1 : 24.5.  Eight heads need
+// two blocks of columns: 92.4 : 67.7.  e4m3 digits (two e4m3 numbers): attention
+// at G = 1, 4, 8 70.6 : 66.0, 72.5 : 71.0, 96.1 : 73.0, and weights to 2^-8 only.
 //
 // The tile is stored in lines of 128 bytes whose 16-byte pieces are swizzled as
 // TMA does (piece i of line r at i ^ (r & 7)); with gq = lane / 4, c4 = lane % 4:

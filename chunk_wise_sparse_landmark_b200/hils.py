@@ -321,7 +321,7 @@ def _rows(t: torch.Tensor, shape, dtype, at: int):
 def _launch(at: int, fn, *args, stream):
     """fn(*args, stream) on CUDA device `at` (its current stream if None)."""
     raw = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() != at:
+    if torch._C._cuda_getDevice() != at:
         with torch.cuda.device(at):
             st = fn(*args, raw)
     else:
