@@ -470,26 +470,31 @@ cudaError_t go_append(const Shape& s, const CacheView& cv, const DecView& dv, co
 HILS_DI float decode1(int8_t c) { return (float)c; }
 HILS_DI float decode1(__nv_fp8_e4m3 c) { return (float)c; }
 
-// 32 bytes, a whole sector, at once
-HILS_DI void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// 32 bytes: a whole sector at once where the output is aligned to it
+HILS_DI void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
-HILS_DI void store16(float* p, const float (&x)[16]) {
+HILS_DI void store16(float* p, const float (&x)[16], bool wide) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
-    store32(p + 8 * h, w);
+    store32(p + 8 * h, w, wide);
   }
 }
-HILS_DI void store16(__nv_bfloat16* p, const float (&x)[16]) {
+HILS_DI void store16(__nv_bfloat16* p, const float (&x)[16], bool wide) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-  store32(p, w);
+  store32(p, w, wide);
 }
 
 // One CTA per (chunk, KV head, sequence; keys or values): a tile is contiguous
@@ -528,6 +533,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView
   }
   const C* page = (const C*)(vals ? cv.v_pool : cv.k_pool) + off;
   const float scale = __ldg((vals ? cv.v_scale : cv.k_scale) + off / (s.S * s.d));
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll 2
   for (int e = threadIdx.x * 16; e < n; e += kThreads * 16) {
     const uint4 w = __ldg(reinterpret_cast<const uint4*>(page + e));
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView
     const C* codes = reinterpret_cast<const C*>(&w);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = decode1(codes[i]) * scale;
-    store16(out + e, x);
+    store16(out + e, x, wide);
   }
 }
 

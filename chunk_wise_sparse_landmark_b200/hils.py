@@ -583,6 +583,7 @@ class CacheDecode:
         assert seq_lens.shape == (B,) and block_table.shape[0] == B
         self.seq_lens, self.block_table = seq_lens, block_table
         self.paged = paged(seq_lens, block_table, num_pages)
+        assert fmt in self._POOL, f"fmt is one of {tuple(self._POOL)}"
         el = self._POOL[fmt] or dt
         pools = [torch.zeros((num_pages, Hkv, S, d), dtype=el, device=dev) for _ in range(2)]
         rest = []

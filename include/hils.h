@@ -301,10 +301,12 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
  * the tokens were split over calls, and a sequence may be cut back by the
  * tokens of its last chunk and the one before (its length reduced, other
  * tokens appended) as long as every token of those two chunks was appended
- * here.  8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
+ * here.  A sequence that begins with pages of another one (a shared prefix)
+ * begins its own appends at a chunk's first token.  8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
  * and dtype BF16 with d = 128, S = 64, and pools of up to 256 GB; native caches every shape of the
  * summaries (hils_attn_decode_cache: those of hils_attn_decode_paged).
- * Pools, tails and scales are 16-byte aligned.
+ * Pools, tails and scales are 16-byte aligned device memory; scales are >= 0 or
+ * NaN.
  */
 typedef enum { HILS_KV_NATIVE = 0, HILS_KV_I8 = 1, HILS_KV_E4M3 = 2 } hils_kv_format_t;
 

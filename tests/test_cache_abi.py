@@ -144,3 +144,10 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
             H.hils_cache_append(other, pg, c, k, k)
     with pytest.raises(AssertionError):
         H.hils_cache_append(cfg, H.Paged(P, P, 2, 5), c, k, k)  # a table of more pages than the pool has
+
+
+def test_capacities_and_pools_past_the_kernels_ranges():
+    cfg = config(N=2 ** 31 - 10)
+    for name in CALLS:
+        assert call(name, cfg, pg=H.Paged(P, P, 2 ** 25, 100), rows=rows()) == UNSUPPORTED
+        assert call(name, config(), pg=H.Paged(P, P, 16, 2 ** 25), rows=rows()) == UNSUPPORTED  # 2^32 lines of 128 bytes

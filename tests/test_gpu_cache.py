@@ -297,6 +297,54 @@ def test_views_of_one_projection_head_major_output_and_in_place_queries():
     assert same(dev[:, :4], want) and same(dev[:, 4:], qkv[:, 4:])
 
 
+def offset(t):
+    """A copy on the GPU that begins 16 bytes behind a 512-byte border."""
+    n = 16 // t.element_size()
+    store = torch.zeros(t.numel() + n, dtype=torch.uint8 if t.dtype is E4 else t.dtype, device=DEV)
+    view = store[n:].view(t.dtype).view(t.shape)
+    view.copy_(t)
+    assert view.data_ptr() % 32 == 16
+    return view
+
+
+@pytest.mark.parametrize("shape,code", [((BF, 128, 64), I8), ((BF, 128, 64), E4), ((F32, 64, 32), I8), ((BF, 128, 64), None)],
+                         ids=["bf16-i8", "bf16-e4m3", "f32-i8", "native"])
+def test_every_tensor_at_16_byte_alignment(shape, code):
+    dtype, d, S = shape
+    lens = [3 * S + 5, 2 * S]
+    n = sum(lens)
+    c = Case(2, 4, 2, d, S, 4 * S, dtype, code, W=S, K=2)
+    c.dev = [[offset(t) for t in ts] for ts in c.dev]
+    (kp, vp), (ks, vs), (kt, vt) = c.dev
+    c.cache = H.cache(kp, vp, ks, vs, kt, vt) if code else H.cache(kp, vp)
+    angles, _ = c.rope(d, False)
+    rope = H.rope(offset(angles[0]), offset(angles[1]))
+    k, v, q = c.rand(n, 2, d), c.rand(n, 2, d), c.rand(n, 4, d)
+    q_out = offset(torch.zeros_like(q))
+    start = torch.tensor([0, lens[0], n], dtype=torch.int32, device=DEV)
+    H.hils_cache_append(c.cfg, c.paged(lens), c.cache, offset(k), offset(v), offset(q), q_out, rope, start)
+    pos = torch.cat([torch.arange(L) for L in lens])
+    c.ref.append(lens, lens, rotate(k, angles[0][pos], angles[1][pos], False), v)
+    c.check()
+    assert same(q_out, rotate(q, angles[0][pos], angles[1][pos], False))
+    read = [offset(torch.zeros((2, 2, 4 * S, d), dtype=dtype)) for _ in range(2)]
+    H.hils_cache_read(c.cfg, c.paged(lens), c.cache, *read)
+    ql, q1 = c.rand(2, 4, 4, d), c.rand(2, 4, d)
+    blank = torch.full((2, 4, 4, d), 3.0, dtype=dtype), torch.full((2, 4, 4), 3.0)
+    k_sum, b_sum = offset(blank[0]), offset(blank[1])
+    H.hils_build_summaries_cache(c.cfg, c.paged(lens), c.cache, offset(ql), k_sum, b_sum)
+    check_summaries(c, lens, [0, 0], lambda b, ch: ql[b][:, list(ch)].double(), k_sum, b_sum, *blank)
+    for b, L in enumerate(lens):
+        assert same(read[0][b, :, :L], c.ref.values(0, b, L).float().to(dtype))
+        assert same(read[1][b, :, :L], c.ref.values(1, b, L).float().to(dtype)) and (read[1][b, :, L:] == 0).all()
+    if code:
+        idx, s_sel = c.lists(lens)
+        out = offset(torch.zeros((2, 4, d), dtype=dtype))
+        H.hils_attn_decode_cache(c.cfg, offset(q1), c.paged(lens), c.cache, offset(idx), offset(s_sel), out)
+        H.hils_sync_status()
+        c.check_attention(lens, q1, idx, s_sel, out)
+
+
 def test_padded_rows_are_neither_read_nor_written():
     c = Case(3, 4, 1, 128, 64, 300, BF, E4)
     angles, rope = c.rope(128, True)
