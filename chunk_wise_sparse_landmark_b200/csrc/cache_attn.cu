@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
   };
   struct Unit {
     int b, g, c, tile;
-    float ks;
+    float ks;  // filled in by scale_of, behind the tile's fetch
   };
   auto unit_of = [&](int i) {
     Unit x;
@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
     x.g = __shfl_sync(0xffffffffu, my_g, i & 31);
     x.c = __shfl_sync(0xffffffffu, my_c, i & 31);
     x.tile = __shfl_sync(0xffffffffu, my_tile, i & 31);
-    x.ks = __shfl_sync(0xffffffffu, my_scale, i & 31);
     return x;
   };
+  auto scale_of = [&](int i) { return __shfl_sync(0xffffffffu, my_scale, i & 31); };
   const int row = Ops::row_head(gq);
   auto ask_query = [&](const Unit& x, RawRow<T, D>& raw) {
     raw.load(row < G ? q_lmk + ls.of(x.b, x.g * G + row, x.c) : (const T*)nullptr, c4);
@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
   if (u + step < units) {
     next = unit_of(1);
     ask_half(next.tile);
+    next.ks = scale_of(1);
   }
+  now.ks = scale_of(0);
   bool alive = true;
   int i = 0;
   for (; u < units; u += step, ++i) {
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
     if (more2) {
       if (((i + 2) & 31) == 0) look_up(u + 2 * step);
       later = unit_of(i + 2);
+      later.ks = scale_of(i + 2);
     }
     typename Ops::Query q;
     Ops::template make_query<T>(raw, gq, c4, q);
@@ -323,16 +326,21 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
     if (!__all_sync(0xffffffffu, alive)) break;
     {
       const Tile<D, S> t{{buf.h[s0], buf.h[s1]}};
-      float sc[R][S / 8], o[R][N8], inv[R];
+      float sc[R][S / 8], o[R][N8], inv[R], zs[R], zls[R];
       Ops::scores(t, at, q, sc);
       const long long h0 = (long long)now.b * s.Hq + now.g * G;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int h = Ops::head(r, c4);
-        float top, z, zl;
-        weigh<Ops>(sc[r], s.scale * now.ks * q.up[r], top, z, &zl);
-        inv[r] = __fdividef(now.ks, z);
-        if (h < G && gq == 0 && now.tile >= 0) b_sum[(h0 + h) * s.C + now.c] = logf(z * (1.f / Ops::kOne)) - __fdividef(zl, z);
+        float top;
+        weigh<Ops>(sc[r], s.scale * now.ks * q.up[r], top, zs[r], &zls[r]);
+        inv[r] = __fdividef(now.ks, zs[r]);
+      }
+      // lane gq = r of a column writes the entropy of its head r: log l - (sum of weight x) / l
+      if (gq < R) {
+        const int h = Ops::head(gq, c4);
+        const float z = gq == 0 ? zs[0] : zs[R - 1], zl = gq == 0 ? zls[0] : zls[R - 1];
+        if (h < G && now.tile >= 0)
+          b_sum[(h0 + h) * s.C + now.c] = kLn2 * __log2f(z * (1.f / Ops::kOne)) - __fdividef(zl, z);
       }
       Ops::values(t, at, gq, sc, o, [&] {
         __syncwarp();  // every lane has read the first half
