@@ -13,14 +13,14 @@ For summaries and attention let mag = sum of weight * |value| (from the model):
   * float32 inputs: queries are held as two halves, within 2^-22 of themselves,
     which a factor of two on the logits' bound covers; weights within 2^-22, or
     2^-40 of the largest of their chunk (low = sum of that largest * |value|);
-  * bf16 inputs, int8 codes: queries within 1.02 2^-24 of their row's largest
-    element (fixed point, half a step is 1 / 16646144), so a logit within that
-    times wide = max |q| sum |k_e| scale; weights within 1.02 2^-16 of their
-    chunk's largest (half a step is 1 / 65024); the result rounds to bf16 (2^-8
-    of itself);
-  * bf16 inputs, e4m3 codes: queries exact, or within 2^-17 of their row's largest
-    element (two e4m3 numbers, the largest in [2^7, 2^8), the smallest step
-    2^-9); weights within 2^-8 of themselves (2^-4 twice), or 2^-18 of the largest.
+  * bf16 inputs, half precision (e4m3 codes; int8 codes with eight heads in a
+    group): queries exact, or within 2^-39 of their row's largest element, which
+    2^-24 big covers; weights within 2^-11, or 2^-40 of the largest of their chunk;
+    the result rounds to bf16 (2^-8 of itself);
+  * bf16 inputs, int8 digits (up to four heads): queries within 1.02 2^-24 of their
+    row's largest element (fixed point, half a step is 1 / 16646144), so a logit
+    within that times wide = max |q| sum |k_e| scale; weights within 1.02 2^-16 of
+    their chunk's largest (half a step is 1 / 65024).
 """
 import math
 
@@ -46,7 +46,7 @@ def weights_off(dtype, code, d, S, n, big, wide):
         return off, 0.0
     if dtype is F32:
         return off + 2.0 ** -22, 2.0 ** -40
-    return (off + 2 * FIXED_Q * wide, FIXED_P) if code is I8 else (off + 2 * 2.0 ** -17 * wide + 2.0 ** -8, 2.0 ** -18)
+    return (off + 2 * FIXED_Q * wide + 2.0 ** -11, FIXED_P) if code is I8 else (off + 2.0 ** -11, 2.0 ** -40)
 
 
 def out_off(dtype, got, want, mag, low, off):
@@ -526,8 +526,8 @@ def check_summaries(c, lens, first, q_lmk, k_sum, b_sum, blank_k, blank_b):
         # H(p) = -sum p log p: each p off by `eps` of itself moves it by at most eps (H + 1), and log and exp of
         # arguments up to `big` by 2^-22 of them; the entropy's p are not rounded to digits
         eps = 2 * 2 * (c.d + 4) * 2.0 ** -24 * big + 2.0 ** -20 + (c.S + 16) * 2.0 ** -24
-        if c.dtype is BF and c.code is not None:
-            eps += 2 * (FIXED_Q if c.code is I8 else 2.0 ** -17) * wide
+        if c.dtype is BF and c.code is I8:
+            eps += 2 * FIXED_Q * wide
         off = (b_sum[b][:, first[b]:C].double().cpu() - ent).abs()
         assert (off <= eps * (ent + 1) + 2.0 ** -22 * big).all(), (b, off.max())
 
