@@ -408,15 +408,6 @@ HILS_DI void row8(const float* p, float (&x)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-HILS_DI void row8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_f32x2(r[i]);
-    x[2 * i] = f.x, x[2 * i + 1] = f.y;
-  }
-}
 
 // 16 keys of a tail, with the arithmetic of float32: scores sc[r][hi] of key
 // gq + 8 hi and head Ops::head(r, c4), and acc += weights . values (dims gq D / 8 + x).

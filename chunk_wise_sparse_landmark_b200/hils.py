@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -124,6 +125,10 @@ class Rows(ctypes.Structure):
         ("positions", ctypes.c_void_p),
         ("n_rows", ctypes.c_int32),
     ]
+
+
+_ROWS = struct.Struct("4P8q2Pi4x")  # the same as bytes, cheaper to make for a call
+assert _ROWS.size == ctypes.sizeof(Rows)
 
 
 class Rope(ctypes.Structure):
@@ -318,15 +323,18 @@ def _rows(t: torch.Tensor, shape, dtype, at: int):
     return t.data_ptr(), row, head
 
 
-def _launch(at: int, fn, *args, stream):
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _launch(at: int, stream, fn, *args):
     """fn(*args, stream) on CUDA device `at` (its current stream if None)."""
-    raw = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() != at:
+    raw = _raw_stream(at) if stream is None else stream.cuda_stream
+    if _device() != at:
         with torch.cuda.device(at):
             st = fn(*args, raw)
     else:
         st = fn(*args, raw)
-    if st != HILS_OK:
+    if st:
         _check(st)
 
 
@@ -387,7 +395,7 @@ def hils_cache_append(cfg: Config, pg: Paged, cache: Cache, k, v, q=None, q_out=
     """Rotate and append: k, v [n, Hkv, d], q and q_out [n, Hq, d] (views with contiguous heads);
     row_start [B + 1] and positions [n] int32."""
     _cache_fits(cfg, pg, cache)
-    at, el, n, d = cache.at, cache.elements, k.shape[0], cfg.head_dim
+    at, el, n, d = cache.at, cache.elements, k.size(0), cfg.head_dim
     shape = (n, cfg.n_kv_heads, d)
     k, k_row, k_head = _rows(k, shape, el, at)
     v, v_row, v_head = _rows(v, shape, el, at)
@@ -397,14 +405,13 @@ def hils_cache_append(cfg: Config, pg: Paged, cache: Cache, k, v, q=None, q_out=
         shape = (n, cfg.n_q_heads, d)
         qa, q_row, q_head = _rows(q, shape, el, at)
         oa, o_row, o_head = _rows(q_out, shape, el, at)
-    start = None if row_start is None else _t(row_start, (cfg.batch + 1,), torch.int32, at)
-    pos = None if positions is None else _t(positions, (n,), torch.int32, at)
-    r = Rows(k, v, qa, oa, k_row, k_head, v_row, v_head, q_row, q_head, o_row, o_head, start, pos, n)
+    start = 0 if row_start is None else _t(row_start, (cfg.batch + 1,), torch.int32, at)
+    pos = 0 if positions is None else _t(positions, (n,), torch.int32, at)
+    r = _ROWS.pack(k, v, qa, oa, k_row, k_head, v_row, v_head, q_row, q_head, o_row, o_head, start, pos, n)
     if rope is not None:
         assert rope.at == at, "the angle tables are on another device than the cache"
         rope = _at(rope)
-    _launch(at, load().hils_cache_append, _at(cfg), _at(pg), _at(cache), _at(r),
-            rope, stream=stream)
+    _launch(at, stream, load().hils_cache_append, _at(cfg), _at(pg), _at(cache), r, rope)
 
 
 def hils_build_summaries_cache(cfg: Config, pg: Paged, cache: Cache, q_lmk, k_sum, b_sum, from_lens=None, stream=None):
@@ -416,9 +423,9 @@ def hils_build_summaries_cache(cfg: Config, pg: Paged, cache: Cache, q_lmk, k_su
     lmk, shape = {4: (HILS_LMK_CHUNK, (B, hq, C, d)), 3: (HILS_LMK_SEQUENCE, (B, hq, d)),
                   2: (HILS_LMK_SHARED, (hq, d))}[q_lmk.ndim]
     el = cache.elements
-    _launch(at, load().hils_build_summaries_cache, _at(cfg), _at(pg), _at(cache),
+    _launch(at, stream, load().hils_build_summaries_cache, _at(cfg), _at(pg), _at(cache),
             _t(q_lmk, shape, el, at), lmk, None if from_lens is None else _t(from_lens, (B,), torch.int32, at),
-            _t(k_sum, (B, hq, C, d), el, at), _t(b_sum, (B, hq, C), torch.float32, at), stream=stream)
+            _t(k_sum, (B, hq, C, d), el, at), _t(b_sum, (B, hq, C), torch.float32, at))
 
 
 def hils_attn_decode_cache(cfg: Config, q, pg: Paged, cache: Cache, idx, s_sel, out, workspace=None, stream=None):
@@ -430,9 +437,9 @@ def hils_attn_decode_cache(cfg: Config, q, pg: Paged, cache: Cache, idx, s_sel, 
         assert workspace.get_device() == at and workspace.is_contiguous()
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     row = (B, hq, cfg.head_dim)
-    _launch(at, load().hils_attn_decode_cache, _at(cfg), _t(q, row, el, at), _at(pg),
+    _launch(at, stream, load().hils_attn_decode_cache, _at(cfg), _t(q, row, el, at), _at(pg),
             _at(cache), _t(idx, (B, cfg.n_kv_heads, K), torch.int32, at),
-            _t(s_sel, (B, hq, K), torch.float32, at), _t(out, row, el, at), ws, ws_bytes, stream=stream)
+            _t(s_sel, (B, hq, K), torch.float32, at), _t(out, row, el, at), ws, ws_bytes)
 
 
 def hils_cache_read(cfg: Config, pg: Paged, cache: Cache, k_out=None, v_out=None, stream=None):
@@ -442,8 +449,8 @@ def hils_cache_read(cfg: Config, pg: Paged, cache: Cache, k_out=None, v_out=None
     assert some is not None and some.ndim == 4, "k_out or v_out [B, Hkv, rows, d] is needed"
     shape = (cfg.batch, cfg.n_kv_heads, some.shape[2], cfg.head_dim)
     k, v = (None if t is None else _t(t, shape, cache.elements, cache.at) for t in (k_out, v_out))
-    _launch(cache.at, load().hils_cache_read, _at(cfg), _at(pg), _at(cache), k, v,
-            some.shape[2], stream=stream)
+    _launch(cache.at, stream, load().hils_cache_read, _at(cfg), _at(pg), _at(cache), k, v,
+            some.shape[2])
 
 
 def _ph(t: torch.Tensor):
