@@ -376,27 +376,25 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
 }
 
 // ------------------------------------------------------------ cluster access ---
-HILS_DI void cluster_sync() {
+HILS_DI void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-HILS_DI uint32_t peer_addr(const float* p, int rank) {
+HILS_DI void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// into the shared memory of the cluster's first CTA, where `p` is in this one's
+HILS_DI void store_first(float* p, float x) {
   uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
-HILS_DI float peer_f32(const float* p, int rank) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(peer_addr(p, rank)) : "memory");
-  return x;
-}
-HILS_DI float4 peer_f32x4(const float* p, int rank) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(peer_addr(p, rank))
+HILS_DI void store_first(float* p, const float4& x) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
                : "memory");
-  return x;
 }
 // A running maximum starts at -inf and is compared as no less than kLeast, so
 // that e^{a - M} is 0 for a = -inf (and NaN for a NaN) without a case of its own.
@@ -528,6 +526,15 @@ struct TailSlice<__nv_bfloat16, Ops, D> {
 constexpr int kMaxUnits = 64 + 32;  // K list entries, W / S window chunks
 constexpr int kMaxCtas = 8;         // of a cluster
 constexpr int kMaxWarps = 12;       // 16 KB of buffers each at d = 128, S = 64, up to 170 registers a thread
+constexpr int kMaxWarpsOfMany = 10;  // beside the records of a cluster's CTAs
+// a CTA's record: sums [G][D], then for each head its reference and denominator;
+// whole 16-byte pieces
+template <int D, int G>
+constexpr int record_floats() { return G * D + (2 * G + 3) / 4 * 4; }
+template <int D, int S, int G>
+constexpr size_t attn_smem(int nwarp, int ncta) {
+  return sizeof(WarpBuffers<D, S>) * nwarp + 1024 + (ncta > 1 ? sizeof(float) * record_floats<D, G>() * ncta : 0);
+}
 
 // A cluster of CTAs serves one (sequence, KV head).  Units, dealt to the
 // cluster's warps in turn: 16-key slices of the incomplete chunk (from the tail),
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[kMaxWarps][2];
   __shared__ int u_tile[kMaxUnits], u_slot[kMaxUnits], n_units;
-  __shared__ float red_m[kMaxWarps][G], red_d[kMaxWarps][G], cta_m[G], cta_d[G];
+  __shared__ float red_m[kMaxWarps][G], red_d[kMaxWarps][G];
   unsigned char* smem = align_1k(smem_raw);
   const int nwarp = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c4 = lane & 3;
   const int rank = blockIdx.x % ncta, g = (int)(blockIdx.x / ncta) % s.Hkv, b = (int)(blockIdx.x / ncta) / s.Hkv;
@@ -577,6 +584,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     if (rank == 0 && threadIdx.x == 0) raise_status(ctx, kStatusBadIndex);
     return;
   }
+  if (ncta > 1) cluster_arrive();  // waited for before the first CTA's memory is used
   const int cur = (L - 1) / S, wc0 = max(0, cur - s.nw + 1);
   const int n_full = L / S - wc0, part = L % S, n_tail = (part + 15) / 16;
   if (warp == 0) {
@@ -755,7 +763,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   __syncthreads();  // every warp's copies have landed and been read: the buffers now hold the records
 
   float* rec = reinterpret_cast<float*>(smem);
-  float* cta = rec + nwarp * G * D;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int h = Ops::head(r, c4);
@@ -770,6 +777,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     }
   }
   __syncthreads();
+  // the records of a cluster's CTAs, in its first one, behind the warps' buffers
+  float* records = reinterpret_cast<float*>(smem + sizeof(WarpBuffers<D, S>) * nwarp);
+  float* mine = records + rank * record_floats<D, G>();
+  if (ncta > 1) cluster_wait();  // every CTA of the cluster has started
   T* o0 = out + ((long long)b * s.Hq + g * G) * D;
   // four dims of a head at a time
   auto add = [](float4& n, float f, const float4& x) {
@@ -797,39 +808,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     if (ncta == 1) {
       write(x, num, dd);
     } else {
-      *reinterpret_cast<float4*>(cta + x) = num;
+      store_first(mine + x, num);
       if (x % D == 0) {
-        cta_m[h] = Mx;
-        cta_d[h] = dd;
+        store_first(mine + G * D + 2 * h, Mx);
+        store_first(mine + G * D + 2 * h + 1, dd);
       }
     }
   }
   if (ncta == 1) return;
-  cluster_sync();
-  for (int x = 4 * (rank * blockDim.x + threadIdx.x); x < G * D; x += 4 * ncta * blockDim.x) {
+  cluster_arrive();
+  cluster_wait();
+  if (rank > 0) return;
+  for (int x = 4 * threadIdx.x; x < G * D; x += 4 * blockDim.x) {
     const int h = x / D;
-    // all of the other CTAs' records at once
-    float m[kMaxCtas], d[kMaxCtas], Mx = kLeast, dd = 0.f;
-    float4 n[kMaxCtas], num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Mx = kLeast, dd = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kMaxCtas; ++w) {
-      const int from = w < ncta ? w : 0;
-      m[w] = peer_f32(&cta_m[h], from);
-      d[w] = peer_f32(&cta_d[h], from);
-      n[w] = peer_f32x4(cta + x, from);
-    }
-#pragma unroll
-    for (int w = 0; w < kMaxCtas; ++w) Mx = w < ncta ? fmaxf(Mx, m[w]) : Mx;
+    for (int w = 0; w < kMaxCtas; ++w)
+      if (w < ncta) Mx = fmaxf(Mx, records[w * record_floats<D, G>() + G * D + 2 * h]);
 #pragma unroll
     for (int w = 0; w < kMaxCtas; ++w) {
       if (w >= ncta) continue;
-      const float f = exp_neg(m[w] - Mx);
-      add(num, f, n[w]);
-      dd = fmaf(f, d[w], dd);
+      const float* r = records + w * record_floats<D, G>();
+      const float f = exp_neg(r[G * D + 2 * h] - Mx);
+      add(num, f, *reinterpret_cast<const float4*>(r + x));
+      dd = fmaf(f, r[G * D + 2 * h + 1], dd);
     }
     write(x, num, dd);
   }
-  cluster_sync();  // no CTA leaves while its records are read
 }
 
 template <typename T, typename C, int D, int S, int G>
@@ -868,9 +874,11 @@ cudaError_t go_native(const Shape& s, const CacheView& cv, const DecView& dv, co
 template <typename T, typename C, int D, int S, int G>
 cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const DecView& dv, const int32_t* idx,
                     const float* s_sel, void* out, cudaStream_t st, const DevCtx& ctx) {
-  static_assert(2 * sizeof(float) * G * D <= sizeof(WarpBuffers<D, S>), "a warp's record and the CTA's fit the buffers");
+  static_assert(sizeof(float) * G * D <= sizeof(WarpBuffers<D, S>), "a warp's record fits its buffers");
   auto kern = attn_codes_kernel<T, C, D, S, G>;
-  cudaError_t e = ensure_dynamic_smem((const void*)kern, (int)(sizeof(WarpBuffers<D, S>) * kMaxWarps + 1024));
+  cudaError_t e = ensure_dynamic_smem((const void*)kern, (int)(attn_smem<D, S, G>(kMaxWarps, 1) > attn_smem<D, S, G>(kMaxWarpsOfMany, kMaxCtas)
+                                                               ? attn_smem<D, S, G>(kMaxWarps, 1)
+                                                               : attn_smem<D, S, G>(kMaxWarpsOfMany, kMaxCtas)));
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)dv.num_pages * s.Hkv * (S * D / 128);
@@ -890,8 +898,9 @@ cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const De
   share = share < 3 ? 4 : share;
   share = share < units ? share : units;
   int nwarp = (share + ncta - 1) / ncta;
-  nwarp = nwarp > kMaxWarps ? kMaxWarps : nwarp;
-  return launch_overlapped(kern, dim3((unsigned)groups * ncta), nwarp * 32, sizeof(WarpBuffers<D, S>) * nwarp + 1024, ncta,
+  const int most = ncta > 1 ? kMaxWarpsOfMany : kMaxWarps;
+  nwarp = nwarp > most ? most : nwarp;
+  return launch_overlapped(kern, dim3((unsigned)groups * ncta), nwarp * 32, attn_smem<D, S, G>(nwarp, ncta), ncta,
                            st, km, vm, s, (const T*)q, cv, dv, idx, s_sel, (T*)out, ncta, ctx);
 }
 
