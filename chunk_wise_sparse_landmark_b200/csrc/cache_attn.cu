@@ -158,6 +158,19 @@ HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = 
   if (zl) *zl = column_sum(z) * kLn2;
 }
 
+// A block's scale over a sum of weights (up to 2^21) may fall below the normal
+// range where the block's values do not: such a scale is multiplied by 2^40 and the
+// block's sums by 2^-40.
+template <int R, int N>
+HILS_DI float lift(float scale, float (&o)[R][N]) {
+  if (fabsf(scale) >= 0x1p-90f || scale != scale) return scale;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int x = 0; x < N; ++x) o[r][x] *= 0x1p-40f;
+  return scale * 0x1p40f;
+}
+
 // Warps take the chunks of all sequences in turn, so that short and long
 // sequences share the work evenly.  A CTA serves sequences [kSeqs blockIdx.y, +
 // kSeqs): their numbers of chunks are summed up in shared memory, and unit u is
@@ -326,14 +339,13 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
     if (!__all_sync(0xffffffffu, alive)) break;
     {
       const Tile<D, S> t{{buf.h[s0], buf.h[s1]}};
-      float sc[R][S / 8], o[R][N8], inv[R], zs[R], zls[R];
+      float sc[R][S / 8], o[R][N8], zs[R], zls[R];
       Ops::scores(t, at, q, sc);
       const long long h0 = (long long)now.b * s.Hq + now.g * G;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float top;
         weigh<Ops>(sc[r], s.scale * now.ks * q.up[r], top, zs[r], &zls[r]);
-        inv[r] = __fdividef(now.ks, zs[r]);
       }
       // lane gq = r of a column writes the entropy of its head r: log l - (sum of weight x) / l
       if (gq < R) {
@@ -346,13 +358,15 @@ __global__ void __launch_bounds__(kWarps * 32, summary_ctas<T>()) code_summaries
         __syncwarp();  // every lane has read the first half
         if (more) ask_half(next.tile);
       });
+      const float ks = lift(now.ks, o);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = Ops::head(r, c4);
+        const float inv = __fdividef(ks, zs[r]);
         if (h >= G || now.tile < 0) continue;
         T* dst = k_sum + ((h0 + h) * s.C + now.c) * D + gq * N8;
 #pragma unroll
-        for (int x = 0; x < N8; ++x) o[r][x] *= inv[r];
+        for (int x = 0; x < N8; ++x) o[r][x] *= inv;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
           for (int x = 0; x < N8; x += 8)
@@ -710,7 +724,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     const int u = i - n_tail, next = i + step < end ? u_tile[u + step] : -1;
     const bool chosen = u_slot[u] >= 0;
     const float ks = __shfl_sync(0xffffffffu, my_ks, n_done), vs = __shfl_sync(0xffffffffu, my_vs, n_done);
-    float sc[R][S / 8], o[R][N8], fo[R], fu[R];
+    float sc[R][S / 8], o[R][N8], fo[R], fu[R], ls[R];
     alive = mbar_wait(&bar[0], phase[0], ctx);
     if (!__all_sync(0xffffffffu, alive)) break;
     flying[0] = false;
@@ -725,11 +739,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     for (int r = 0; r < R; ++r) {
       float top, l;
       weigh<Ops>(sc[r], s.scale * ks * qr.up[r], top, l);
+      ls[r] = chosen ? l : Ops::kOne;
       // a chosen chunk weighs e^{s^} whatever its l; a window chunk e^{top} l
       const float mine = n_done < 8 ? my_s[r][0] : n_done < 16 ? my_s[r][1] : my_s[r][2];
       const float shat = __shfl_sync(0xffffffffu, mine, 4 * (n_done & 7) + c4);
       fold(r, chosen ? shat : top, chosen ? 1.f : l * (1.f / Ops::kOne), fo[r], fu[r]);
-      fu[r] *= chosen ? __fdividef(vs, l) : vs * (1.f / Ops::kOne);
     }
     alive = mbar_wait(&bar[1], phase[1], ctx);
     if (!__all_sync(0xffffffffu, alive)) break;
@@ -741,6 +755,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
       if (lane == 0) fetch_tile<D, S>(buf.b, &vmap, next, &bar[1], ctx);
       flying[1] = true;
     }
+    const float lifted = lift(vs, o);
+#pragma unroll
+    for (int r = 0; r < R; ++r) fu[r] *= __fdividef(lifted, ls[r]);
     bool same = true;  // no column's maximum moved
 #pragma unroll
     for (int r = 0; r < R; ++r) same = same && fo[r] == 1.f;

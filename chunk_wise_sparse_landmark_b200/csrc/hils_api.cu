@@ -742,6 +742,8 @@ static hils_status_t cache_args(const hils_config_t* cfg, const hils_paged_t* pa
   HILS_TRY(make_shape(cfg, s, cache->format == HILS_KV_NATIVE ? native : kOpCache8));
   if (s->N > 0x7fffffff - s->S)
     return fail(HILS_ERR_UNSUPPORTED, "cache: seq_len %d leaves no room for a whole last chunk in 32 bits", s->N);
+  if (s->B > 65535 || s->Hkv > 32767)
+    return fail(HILS_ERR_UNSUPPORTED, "cache: more than 65535 sequences or 32767 KV heads (B=%d Hkv=%d)", s->B, s->Hkv);
   HILS_TRY(paged_view(*s, paged, dv));
   // the 8-bit kernels address the pool by 128-byte lines in 32 bits
   if (cache->format != HILS_KV_NATIVE &&

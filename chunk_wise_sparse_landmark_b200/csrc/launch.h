@@ -125,7 +125,9 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // returned to the caller; later calls must not find it
+  return e;
 }
 cudaError_t launch_cache_append(const Shape& s, const CacheView& cv, const DecView& dv, const NewRows& rows,
                                 const RopeView& rope, cudaStream_t st, const DevCtx& ctx);

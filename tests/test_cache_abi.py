@@ -151,3 +151,5 @@ def test_capacities_and_pools_past_the_kernels_ranges():
     for name in CALLS:
         assert call(name, cfg, pg=H.Paged(P, P, 2 ** 25, 100), rows=rows()) == UNSUPPORTED
         assert call(name, config(), pg=H.Paged(P, P, 16, 2 ** 25), rows=rows()) == UNSUPPORTED  # 2^32 lines of 128 bytes
+        assert call(name, config(B=65536), rows=rows()) == UNSUPPORTED
+        assert call(name, config(Hq=32768, Hkv=32768), rows=rows()) == UNSUPPORTED

@@ -50,7 +50,9 @@ def weights_off(dtype, code, d, S, n, big, wide):
 
 
 def out_off(dtype, got, want, mag, low, off):
-    tol = mag * off[0] + low * off[1] + (want.abs() * 2.0 ** -8 if dtype is BF else want.abs() * 2.0 ** -24)
+    # the rounding of the result: half a step, which for numbers below 2^-126 is half of bf16's 2^-133 (float32: 2^-149)
+    half = (want.abs() * 2.0 ** -8).clamp(min=2.0 ** -134) if dtype is BF else (want.abs() * 2.0 ** -24).clamp(min=2.0 ** -150)
+    tol = mag * off[0] + low * off[1] + half
     return ((got.double().cpu() - want).abs() - tol).max().item()
 
 
@@ -703,6 +705,78 @@ def test_attention_with_large_and_small_values(dtype):
     H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), out)
     H.hils_sync_status()
     c.check_attention(lens, q, idx, s_sel, out)
+
+
+@pytest.mark.parametrize("dtype,code,G", [(BF, I8, 4), (BF, I8, 8), (BF, E4, 4), (F32, I8, 2)])
+def test_attention_over_blocks_of_zeros_and_queries_of_zeros(dtype, code, G):
+    """Scales of zero (all logits of the block alike, nothing added to the sums), a query of zeros and a tiny one, and
+    a whole context of zeros."""
+    c = Case(2, G, 1, 128, 64, 640, dtype, code, W=128, K=4)
+    lens = [600, 640]
+    k, v = c.rand(1240, 1, 128), c.rand(1240, 1, 128)
+    k[64:128] = 0
+    v[128:192] = 0
+    k[512:540], v[530:560] = 0, 0
+    k[600:], v[600:] = 0, 0
+    c.append(lens, lens, k, v)
+    idx, s_sel = c.lists(lens)
+    idx[0, 0] = torch.tensor([0, 1, 2, 5])
+    q = c.rand(2, G, 128)
+    q[0, 0], q[0, 1] = 0, q[0, 1] * 2.0 ** -120
+    out = torch.full((2, G, 128), math.nan, dtype=dtype, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    H.hils_sync_status()
+    c.check_attention(lens, q, idx, s_sel, out)
+    assert (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("code", [I8, E4], ids=["i8", "e4m3"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_the_smallest_blocks_that_are_held(dtype, code):
+    """Values of 2^-109 to 2^-100: a scale over a sum of weights is below the normal range, the sums are not."""
+    c = Case(1, 8, 2, 128, 64, 640, dtype, code, W=128, K=3)
+    k, v = c.rand(600, 2, 128), c.rand(600, 2, 128)
+    k[:300] *= 2.0 ** -109
+    v *= 2.0 ** -109
+    v[300:] *= 2.0 ** 9
+    c.append([600], [600], k, v)
+    idx, s_sel = c.lists([600])
+    q, ql = c.rand(1, 8, 128), c.rand(1, 8, 10, 128)
+    out = torch.empty((1, 8, 128), dtype=dtype, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged([600]), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    blank = torch.full((1, 8, 10, 128), 3.0, dtype=dtype), torch.full((1, 8, 10), 3.0)
+    k_sum, b_sum = blank[0].to(DEV), blank[1].to(DEV)
+    H.hils_build_summaries_cache(c.cfg, c.paged([600]), c.cache, ql.to(DEV), k_sum, b_sum)
+    H.hils_sync_status()
+    assert (out != 0).all() and (k_sum[:, :, :4] != 0).float().mean() > 0.9
+    c.check_attention([600], q, idx, s_sel, out)
+    check_summaries(c, [600], [0], lambda b, ch: ql[b][:, list(ch)].double(), k_sum, b_sum, *blank)
+
+
+def test_codes_and_scales_that_no_append_makes():
+    """A pool filled elsewhere: codes of -128, scales that are negative, very small and very large."""
+    c = Case(1, 8, 2, 128, 64, 640, BF, I8, W=128, K=6)
+    c.fill([640])
+    for x in range(2):
+        c.ref.pool[x][:, :, ::3, ::5] = -128
+        c.ref.scale[x][int(c.table[0, 1])] = -0.02
+        c.ref.scale[x][int(c.table[0, 2])] = 2.0 ** -130
+    c.ref.scale[1][int(c.table[0, 3])] = 2.0 ** 100
+    for got, want in zip(c.dev, (c.ref.pool, c.ref.scale)):
+        for x in range(2):
+            got[x].copy_(want[x])
+    idx = torch.arange(6, dtype=torch.int32).expand(1, 2, 6).contiguous()
+    s_sel = 3 + c.rand(1, 8, 6).float()
+    q = c.rand(1, 8, 128)
+    out = torch.empty((1, 8, 128), dtype=BF, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged([640]), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    ql = c.rand(1, 8, 10, 128)
+    blank = torch.full((1, 8, 10, 128), 3.0, dtype=BF), torch.full((1, 8, 10), 3.0)
+    k_sum, b_sum = blank[0].to(DEV), blank[1].to(DEV)
+    H.hils_build_summaries_cache(c.cfg, c.paged([640]), c.cache, ql.to(DEV), k_sum, b_sum)
+    H.hils_sync_status()
+    c.check_attention([640], q, idx, s_sel, out)
+    check_summaries(c, [640], [0], lambda b, ch: ql[b][:, list(ch)].double(), k_sum, b_sum, *blank)
 
 
 def test_attention_reads_no_masked_place():
