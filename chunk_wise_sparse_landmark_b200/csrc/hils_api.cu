@@ -779,6 +779,11 @@ hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* pa
                     (long long)st[i]);
     if (rows->q == rows->q_out && rows->q && (st[4] != st[6] || st[5] != st[7]))
       return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: q_out in place needs the strides of q");
+    // written rows: one address, one element (rows of heads or heads of rows)
+    if (rows->q && !((st[7] >= s.d || s.Hq == 1) && (st[6] >= s.d || rows->n_rows == 1)))
+      return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: rows or heads of q_out lie on one another (strides %lld, "
+                                        "%lld, d=%d)",
+                  (long long)st[6], (long long)st[7], s.d);
   }
   RopeView rp;
   if (rope) {
@@ -796,6 +801,8 @@ hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* pa
     rp.interleaved = rope->interleaved;
   }
   if (rows->n_rows == 0) return HILS_OK;
+  if (cv.k_pool == cv.v_pool || (cv.k_scale && (cv.k_scale == cv.v_scale || cv.k_tail == cv.v_tail)))
+    return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: keys and values of the cache share memory");
   NewRows nr{rows->k,      rows->v,      rows->q,     rows->q_out, rows->k_row,     rows->k_head,     rows->v_row,
              rows->v_head, rows->q_row,  rows->q_head, rows->q_out_row, rows->q_out_head, rows->row_start,
              rows->positions, rows->n_rows};
@@ -864,6 +871,7 @@ hils_status_t hils_cache_read(const hils_config_t* cfg, const hils_paged_t* page
   if ((!k_out && !v_out) || (k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)))
     return fail(HILS_ERR_INVALID_ARG, "hils_cache_read: no output, or an unaligned one");
   if (out_rows < 1) return fail(HILS_ERR_INVALID_ARG, "hils_cache_read: out_rows %d < 1", out_rows);
+  if (k_out == v_out) return fail(HILS_ERR_INVALID_ARG, "hils_cache_read: k_out and v_out are the same memory");
   DevCtx ctx;
   HILS_TRY(dev_ctx(&ctx));
   HILS_LAUNCH(launch_cache_read(s, cv, dv, k_out, v_out, out_rows, (cudaStream_t)stream, ctx), "cache_read");

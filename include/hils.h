@@ -340,7 +340,9 @@ typedef struct {
  * elements, from one row / one head to the next (multiples of 16 bytes; the d
  * elements of a head are contiguous), so that k, v and q may be views of one
  * projection's output.  q may be NULL; else its rotated rows go to q_out, which
- * may be q itself with the same strides and overlaps nothing otherwise. */
+ * may be q itself with the same strides and overlaps nothing otherwise; its
+ * own rows and heads lie apart (strides of at least d, those of k, v and q may
+ * be 0). */
 typedef struct {
   const void* k;            /* [n_rows, Hkv, d] dtype */
   const void* v;            /* [n_rows, Hkv, d] */
@@ -393,7 +395,8 @@ hils_status_t hils_attn_decode_cache(const hils_config_t* cfg, const void* q, co
 /* The cache as contiguous rows, e.g. for hils_attn_prefill over a prompt as
  * decode will see it: k_out, v_out [B, Hkv, out_rows, d] (dtype) get at row p
  * the values of position p < min(seq_lens[b], out_rows); other rows are left as
- * they were.  Either output may be NULL.  A length of 0 reads nothing. */
+ * they were.  Either output may be NULL (they are
+ * never the same memory).  A length of 0 reads nothing. */
 hils_status_t hils_cache_read(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
                               void* k_out, void* v_out, int32_t out_rows, void* stream);
 

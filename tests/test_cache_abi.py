@@ -111,6 +111,22 @@ def test_other_arguments_that_are_refused():
     assert b"workspace" in H.load().hils_last_error()
 
 
+def test_outputs_that_lie_on_one_another_are_refused():
+    """Rows or heads of q_out with one address, keys and values of a cache or of a read in the same memory."""
+    apart = H.Cache(P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, H.HILS_KV_I8)
+    for kw in (dict(q_out_row=0), dict(q_out_head=0), dict(q_out_head=64), dict(q_out_row=120)):
+        assert call("append", config(), cache=apart, rows=rows(**kw)) == INVALID
+        assert b"q_out lie on one another" in H.load().hils_last_error(), kw
+    for change in (dict(v_pool=P), dict(v_scale=3 * P), dict(v_tail=5 * P)):
+        c = H.Cache(*[getattr(apart, f) for f, _ in H.Cache._fields_])
+        for f, x in change.items():
+            setattr(c, f, x)
+        assert call("append", config(), cache=c, rows=rows()) == INVALID
+        assert b"share memory" in H.load().hils_last_error(), change
+    assert call("read", config(), cache=apart) == INVALID
+    assert b"same memory" in H.load().hils_last_error()
+
+
 def test_rope_tables():
     """cos and sin of p base^(-2 i / rot) rounded once to float32, also at far positions."""
     cos, sin = H.rope_tables(200000, 32, base=500000.0, device="cpu")
