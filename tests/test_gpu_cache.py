@@ -299,6 +299,27 @@ def test_views_of_one_projection_head_major_output_and_in_place_queries():
     assert same(dev[:, :4], want) and same(dev[:, 4:], qkv[:, 4:])
 
 
+@pytest.mark.parametrize("dtype,d,S", [(BF, 128, 64), (F32, 64, 32)], ids=["bf16", "f32"])
+def test_rows_and_heads_of_stride_zero(dtype, d, S):
+    """One head for all heads (keys, queries), one row for all rows (values)."""
+    c = Case(2, 4, 2, d, S, 5 * S, dtype, E4)
+    (angles, rope), n = c.rope(d, False), 3 * S + 7
+    lens = news = [2 * S, S + 7]
+    k, v, q = c.rand(n, 1, d), c.rand(1, 2, d), c.rand(n, 1, d)
+    pos = torch.cat([torch.arange(x) for x in lens])
+    out = torch.zeros((n, 4, d), dtype=dtype, device=DEV)
+    start = torch.tensor([0, 2 * S, n], dtype=torch.int32, device=DEV)
+    H.hils_cache_append(c.cfg, c.paged(lens), c.cache, k.to(DEV).expand(n, 2, d), v.to(DEV).expand(n, 2, d),
+                        q.to(DEV).expand(n, 4, d), out, rope, start)
+    turn = lambda x: rotate(x, angles[0][pos], angles[1][pos], False)
+    c.ref.append(lens, news, turn(k.expand(n, 2, d)), v.expand(n, 2, d).contiguous())
+    c.check()
+    assert same(out, turn(q.expand(n, 4, d)).contiguous())
+    with pytest.raises(H.HilsError, match="lie on one another"):
+        H.hils_cache_append(c.cfg, c.paged(lens), c.cache, k.to(DEV).expand(n, 2, d), v.to(DEV).expand(n, 2, d),
+                            q.to(DEV).expand(n, 4, d), out[:, :1].expand(n, 4, d), rope, start)
+
+
 def offset(t):
     """A copy on the GPU that begins 16 bytes behind a 512-byte border."""
     n = 16 // t.element_size()
