@@ -421,47 +421,60 @@ HILS_DI void row8(const float* p, float (&x)[8]) {
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// 16 keys of a tail, with the arithmetic of float32: scores sc[r][hi] of key
-// gq + 8 hi and head Ops::head(r, c4), and acc += weights . values (dims gq D / 8 + x).
-// float32 configurations: on CUDA cores.
+// KEYS keys of a tail, with the arithmetic of float32: scores sc[r][x] of key
+// gq + 8 x and head Ops::head(r, c4), and acc += weights . values (dims gq D / 8 + x).
+// float32 configurations: on CUDA cores, eight keys, so that a tail is shared by more
+// warps, and a quarter of a key's dims to a thread (24 sequences of 4K, d = 64, S = 32,
+// G = 4: 7.4 us; sixteen keys 10.3; eight, a key's dims and two heads to a thread 7.9).
 template <typename T, typename Ops, int D>
 struct TailSlice {
-  static constexpr int R = Ops::R, N8 = D / 8;
+  static constexpr int R = Ops::R, N8 = D / 8, KEYS = 8;
+  HILS_DI static void f4(const float* p, float* y) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w;
+  }
   const T *kt, *vt, *q0;
   int nk, heads, gq, c4;
   HILS_DI void load(const T* kt_, const T* vt_, const T* q0_, int nk_, int G, int gq_, int c4_) {
     kt = kt_, vt = vt_, q0 = q0_, nk = nk_, heads = G, gq = gq_, c4 = c4_;
   }
-  HILS_DI void scores(float (&sc)[R][2]) const {
+  // key gq, the dims 16 e + 4 c4 .., + 3, all heads; then the quarters are added
+  HILS_DI void scores(float (&sc)[R][KEYS / 8]) const {
+    const T* kr = kt + min(gq, nk - 1) * D;
+    float x[D / 4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = 0.f;
-#pragma unroll 4
-    for (int e = 0; e < D; e += 8) {
-      float k0[8], k1[8];
-      row8(kt + min(gq, nk - 1) * D + e, k0);
-      row8(kt + min(gq + 8, nk - 1) * D + e, k1);
+    for (int e = 0; e < D / 4; e += 4) f4(kr + 4 * e + 4 * c4, x + e);
+    sc[0][0] = sc[R - 1][0] = 0.f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float qa[8];
-        row8(q0 + min(Ops::head(r, c4), heads - 1) * D + e, qa);
+    for (int h = 0; h < 8; ++h) {
+      if (h >= heads) break;
+      const T* qr = q0 + h * D + 4 * c4;
+      float sum = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          sc[r][0] = fmaf(k0[x], qa[x], sc[r][0]);
-          sc[r][1] = fmaf(k1[x], qa[x], sc[r][1]);
-        }
+      for (int e = 0; e < D / 4; e += 4) {
+        float y[4];
+        f4(qr + 4 * e, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fmaf(x[e + i], y[i], sum);
       }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int r = 0; r < R; ++r) sc[r][0] = h == Ops::head(r, c4) ? sum : sc[r][0];
     }
   }
-  HILS_DI void add_values(const float (&p)[R][2], float (&acc)[R][N8]) const {
-#pragma unroll 4
-    for (int k = 0; k < nk; ++k) {
+  HILS_DI void add_values(const float (&p)[R][KEYS / 8], float (&acc)[R][N8]) const {
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
       float w[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, k < 8 ? p[r][0] : p[r][1], 4 * (k & 7) + c4);
+      for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, p[r][0], 4 * k + c4);
 #pragma unroll
       for (int e = 0; e < N8; e += 8) {
         float v[8];
-        row8(vt + k * D + gq * N8 + e, v);
+        row8(vt + min(k, nk - 1) * D + gq * N8 + e, v);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = k < nk ? v[x] : 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -477,7 +490,7 @@ HILS_DI float bf16_part(float x) { return __bfloat162float(__float2bfloat16_rn(x
 template <typename Ops, int D>
 struct TailSlice<__nv_bfloat16, Ops, D> {
   using T = __nv_bfloat16;
-  static constexpr int R = Ops::R, N8 = D / 8, Q4 = D / 32, V4 = N8 / 8;
+  static constexpr int R = Ops::R, N8 = D / 8, KEYS = 16, Q4 = D / 32, V4 = N8 / 8;
   uint4 k[2][Q4], q[Q4], v[4][V4];
   HILS_DI static uint32_t word(const uint4* x, int i) {
     const uint4& w = x[i >> 2];
@@ -551,7 +564,7 @@ constexpr size_t attn_smem(int nwarp, int ncta) {
 }
 
 // A cluster of CTAs serves one (sequence, KV head).  Units, dealt to the
-// cluster's warps in turn: 16-key slices of the incomplete chunk (from the tail),
+// cluster's warps in turn: slices of the incomplete chunk (from the tail),
 // then the window's complete chunks and the chosen chunks (tiles of codes).  Each
 // warp folds its units with a running maximum per head, the CTA its warps, and
 // the cluster its CTAs through distributed shared memory: one launch, no
@@ -567,7 +580,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Shape s,
     const T* q, CacheView cv, DecView dv, const int32_t* idx, const float* s_sel, T* out, int ncta, DevCtx ctx) {
   using Ops = typename OpsOf<T, C, D, S, G>::type;
-  constexpr int R = Ops::R, N8 = D / 8;
+  using Slice = TailSlice<T, Ops, D>;
+  constexpr int R = Ops::R, N8 = D / 8, KEYS = Slice::KEYS;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[kMaxWarps][2];
   __shared__ int u_tile[kMaxUnits], u_slot[kMaxUnits], n_units;
@@ -600,7 +614,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   }
   if (ncta > 1) cluster_arrive();  // waited for before the first CTA's memory is used
   const int cur = (L - 1) / S, wc0 = max(0, cur - s.nw + 1);
-  const int n_full = L / S - wc0, part = L % S, n_tail = (part + 15) / 16;
+  const int n_full = L / S - wc0, part = L % S, n_tail = (part + KEYS - 1) / KEYS;
   if (warp == 0) {
     // the live units: window chunks, then accepted list entries (the list form, common.cuh)
     bool bad;
@@ -689,26 +703,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
   look_ahead(first);
 
   for (; i < n_tail; i += step) {
-    // keys [16 i, 16 i + 16) of the incomplete chunk, as they are in the tail
-    const long long off = tail_off(s, b, g, cur) + 16 * i * D;
+    // the incomplete chunk's keys from KEYS i on, as they are in the tail
+    const long long off = tail_off(s, b, g, cur) + KEYS * i * D;
     const T* kt = (const T*)cv.k_tail + off;
     const T* vt = (const T*)cv.v_tail + off;
-    const int nk = min(16, part - 16 * i);
-    float sc[R][2];  // keys gq and gq + 8
-    TailSlice<T, Ops, D> slice;
+    const int nk = min(KEYS, part - KEYS * i);
+    float sc[R][KEYS / 8];  // keys gq (and gq + 8)
+    Slice slice;
     slice.load(kt, vt, q0, nk, G, gq, c4);
     slice.scores(sc);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      sc[r][0] = gq < nk ? sc[r][0] * s.scale : -INFINITY;
-      sc[r][1] = gq + 8 < nk ? sc[r][1] * s.scale : -INFINITY;
-      const float top = column_max(fmaxf(sc[r][0], sc[r][1])), m = top == -INFINITY ? 0.f : top;
-      sc[r][0] = exp_neg(sc[r][0] - m);
-      sc[r][1] = exp_neg(sc[r][1] - m);
+      float top = -INFINITY, mass = 0.f;
+#pragma unroll
+      for (int x = 0; x < KEYS / 8; ++x) {
+        sc[r][x] = gq + 8 * x < nk ? sc[r][x] * s.scale : -INFINITY;
+        top = fmaxf(top, sc[r][x]);
+      }
+      top = column_max(top);
+      const float m = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int x = 0; x < KEYS / 8; ++x) {
+        sc[r][x] = exp_neg(sc[r][x] - m);
+        mass += sc[r][x];
+      }
       float fo, fu;
-      fold(r, top, column_sum(sc[r][0] + sc[r][1]), fo, fu);
-      sc[r][0] *= fu;
-      sc[r][1] *= fu;
+      fold(r, top, column_sum(mass), fo, fu);
+#pragma unroll
+      for (int x = 0; x < KEYS / 8; ++x) sc[r][x] *= fu;
 #pragma unroll
       for (int x = 0; x < N8; ++x) acc[r][x] *= fo;
     }
@@ -908,7 +930,8 @@ cudaError_t go_attn(const Shape& s, const void* q, const CacheView& cv, const De
   // Below three a warp's own chain of units is the longer way: 768 with two 102 us,
   // with four 95.  Few of them spread over clusters of CTAs, one multiprocessor
   // each, down to one unit a warp.
-  const int sms = device_sm_count(), groups = s.B * s.Hkv, units = s.K + s.nw + 3;
+  const int sms = device_sm_count(), groups = s.B * s.Hkv;
+  const int units = s.K + s.nw - 1 + S / TailSlice<T, typename OpsOf<T, C, D, S, G>::type, D>::KEYS;
   int ncta = sms / groups;
   ncta = ncta < 1 ? 1 : ncta > kMaxCtas ? kMaxCtas : ncta;
   int share = sms * kMaxWarps / groups;
