@@ -386,6 +386,8 @@ hils_status_t hils_build_summaries_cache(const hils_config_t* cfg, const hils_pa
  * window's complete chunks from the pool, the incomplete chunk from the tail.
  * out rows of sequences with a length outside [1, L_max] (reported) are
  * left as they were for the 8-bit formats, and undefined for native caches.
+ * An infinity or a NaN in a tail makes the outputs that attend it infinite or
+ * NaN, as one in a block of codes makes them NaN.
  * workspace: HILS_WS_ATTN_DECODE for native caches; 8-bit formats need none
  * (NULL, 0). */
 hils_status_t hils_attn_decode_cache(const hils_config_t* cfg, const void* q, const hils_paged_t* paged,
