@@ -126,8 +126,10 @@ struct OpsOf<__nv_bfloat16, CodeI8, D, S, 4> {
 
 // sc (scores) -> weights kOne e^{x - top} of the logits x = sc mul: `top` the
 // column's largest logit, `l` the weights' sum (float32); zl, if wanted, the sum of
-// weight * (x - top).  In the exponent mul log2 e is one factor and top one term,
-// so each weight is off by 2^-23 |x| more, and by no instruction of its own.
+// weight * (x - top).  The largest score is taken off before the scaling: its own
+// exponent is 0 whatever the logits' size, so that no weight is above kOne, which
+// the digits and halves of the products (code_mma.cuh) have little room beyond.  (One
+// instruction a weight: 131072 tokens' summaries 35.2 us for 35.0, attention 81.2 for 80.9.)
 template <typename Ops, int N>
 HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = nullptr) {
   if (mul < 0.f) {  // (a scale of a pool that was filled elsewhere)
@@ -140,17 +142,17 @@ HILS_DI void weigh(float (&sc)[N], float mul, float& top, float& l, float* zl = 
   for (int i = 1; i < N; ++i) m = fmaxf(m, sc[i]);
   m = column_max(m);
   top = m * mul;
-  const float f = mul * kLog2e, c = m == -INFINITY ? 0.f : m * f;
+  const float f = mul * kLog2e, c = m == -INFINITY ? 0.f : m;
   l = 0.f;
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (zl) {
-      const float x = fmaf(sc[i], f, -c);
+      const float x = (sc[i] - c) * f;
       sc[i] = exp2_fast(x + Ops::kLog2One);
       z = fmaf(sc[i], x, z);
     } else {
-      sc[i] = exp2_fast(fmaf(sc[i], f, Ops::kLog2One - c));
+      sc[i] = exp2_fast(fmaf(sc[i] - c, f, Ops::kLog2One));
     }
     l += sc[i];
   }

@@ -1,0 +1,97 @@
+"""The 8-bit paged cache at the ends of its ranges: logits so large that a rounding of theirs is a power of e.
+
+Tolerances are those of test_gpu_cache.py.  Where every softmax of a test gives all its mass to one key, with 100 and
+the logits' own errors between it and the next, an error of a logit moves no weight by more than e^-100, so that
+the terms with the logits' size drop out (big = wide = 0).
+"""
+import math
+
+import pytest
+import torch
+
+from chunk_wise_sparse_landmark_b200 import hils as H
+from tests.cache_ref import attend, summaries
+from tests.test_gpu_cache import BF, DEV, E4, F32, FIXED_Q, I8, Case, out_off, weights_off
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(BF, I8, 1), (BF, I8, 2), (BF, I8, 4), (BF, I8, 8), (BF, E4, 1), (BF, E4, 4), (F32, I8, 2), (F32, E4, 8)]
+FORM_IDS = [f"{'bf16' if t is BF else 'f32'}-{'i8' if c is I8 else 'e4m3'}-G{g}" for t, c, g in FORMS]
+
+
+def one_key_each(c, L, q, k, first=0):
+    """Checks, in 64 bits, that in every chunk of the keys k [L, d] one key takes all of each head's mass."""
+    logit = (k @ q.T) * c.scale
+    wide = (k.abs().sum(dim=1).max() * q.abs().max() * c.scale).item()
+    off = 2 * ((c.d + 4) * 2.0 ** -24 + 2.0 ** -22 + FIXED_Q) * wide
+    for a in range(first, L - L % c.S, c.S):
+        top = logit[a:a + c.S].topk(2, dim=0).values
+        assert (top[0] - top[1] >= 100 + 2 * off).all()
+
+
+def large_keys(c, n, axis, size):
+    """n keys along `axis` [d] of signs; in a chunk all of one sign, sizes 0.4 .. 0.9 times `size`, one of them 1 times
+    (positive) or 0.3 times it (negative): the logits of a query along the axis have one far above the others."""
+    y = size * torch.empty(n).uniform_(0.4, 0.9, generator=c.gen)
+    for a in range(0, n, c.S):
+        m = min(c.S, n - a)
+        at = a + int(torch.randint(m, (1,), generator=c.gen))
+        negative = (a // c.S) % 3 == 2
+        y[at] = (0.3 if negative else 1.0) * size
+        if negative:
+            y[a:a + m] *= -1
+    return y[:, None] * axis
+
+
+@pytest.mark.parametrize("times", [1, 100])
+@pytest.mark.parametrize("dtype,code,G", FORMS, ids=FORM_IDS)
+def test_attention_at_logits_of_ten_thousands_and_more(dtype, code, G, times):
+    """Chosen chunks whose logits are 4e4 .. 2e8 or minus those (over a window of zeros), and a window of such
+    chunks (one key in it is the largest by far)."""
+    B, L, S = 24, 10 * 64 + 5, 64
+    c = Case(B, G, 1, 128, S, 11 * S, dtype, code, W=4 * S, K=6)
+    axis = torch.randint(0, 2, (128,), generator=c.gen).float() * 2 - 1
+    q = ((30 * times * 40 ** torch.rand((B, G, 1), generator=c.gen)) * axis).to(dtype)  # 30 .. 1200, times `times`
+    k = torch.zeros((B, L, 128))
+    for b in range(B):
+        if b % 2 == 0:
+            k[b, :7 * S] = large_keys(c, 7 * S, axis, 130.0)
+        else:
+            k[b] = large_keys(c, L, axis, 65.0)
+            k[b, 7 * S + b] = 130.0 * axis  # the window's largest
+    k = k.reshape(B * L, 1, 128).to(dtype)
+    c.append([L] * B, [L] * B, k, c.rand(B * L, 1, 128))
+    idx = torch.tensor([0, 1, 2, 3, 4, 6], dtype=torch.int32).expand(B, 1, 6).contiguous()
+    s_sel = 3 + torch.randn((B, G, 6), generator=c.gen)
+    out = torch.full((B, G, 128), math.nan, dtype=dtype, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged([L] * B), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    H.hils_sync_status()
+    off = weights_off(dtype, code, 128, S, 10 * S, 0, 0)
+    for b in range(B):
+        kk, vv = c.ref.values(0, b, L), c.ref.values(1, b, L)
+        one_key_each(c, 7 * S, q[b].double(), kk[0, :7 * S])
+        want, mag, low, big, _ = attend(q[b].double(), kk, vv, idx[b].tolist(), s_sel[b].double(), S, c.W, c.scale)
+        assert big >= 4e4
+        assert out_off(dtype, out[b], want, mag, low, off) <= 0, b
+
+
+@pytest.mark.parametrize("times", [1, 100])
+@pytest.mark.parametrize("dtype,code,G", FORMS, ids=FORM_IDS)
+def test_summaries_at_logits_of_ten_thousands_and_more(dtype, code, G, times):
+    """Each chunk's summary is its one key, with an entropy of zero."""
+    C, S = 60, 64
+    c = Case(1, G, 1, 128, S, C * S, dtype, code)
+    axis = torch.randint(0, 2, (128,), generator=c.gen).float() * 2 - 1
+    ql = ((30 * times * 40 ** torch.rand((1, G, C, 1), generator=c.gen)) * axis).to(dtype)
+    k = large_keys(c, C * S, axis, 130.0)[:, None].to(dtype)
+    c.append([C * S], [C * S], k, k)
+    k_sum, b_sum = torch.zeros((1, G, C, 128), dtype=dtype, device=DEV), torch.zeros((1, G, C), device=DEV)
+    H.hils_build_summaries_cache(c.cfg, c.paged([C * S]), c.cache, ql.to(DEV), k_sum, b_sum)
+    H.hils_sync_status()
+    held = c.ref.values(0, 0, C * S)
+    for ch in range(C):
+        one_key_each(c, S, ql[0, :, ch].double(), held[0, ch * S:ch * S + S])
+    want, ent, mag, low = summaries(held.reshape(1, C, S, 128), ql[0].double(), c.scale)
+    assert out_off(dtype, k_sum[0], want, mag, low, weights_off(dtype, code, 128, S, S, 0, 0)) <= 0
+    # the one weight's exponent is 0: log and exp of 1, to 2^-20 each
+    assert (b_sum[0].double().cpu() - ent).abs().max() <= 2.0 ** -19
