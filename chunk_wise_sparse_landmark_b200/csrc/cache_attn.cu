@@ -9,6 +9,8 @@
 // With k_j = a x_j (a the block's scale, x_j codes) the logit is (q.x_j) a scale
 // and the block's output (sum_j p_j y_j) a_v: a scale is applied once for a
 // logit and once for an output element, never to a code.
+#include <cfloat>
+
 #include "code_mma.cuh"
 #include "launch.h"
 
@@ -412,9 +414,10 @@ HILS_DI void store_first(float* p, const float4& x) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
                : "memory");
 }
-// A running maximum starts at -inf and is compared as no less than kLeast, so
-// that e^{a - M} is 0 for a = -inf (and NaN for a NaN) without a case of its own.
-constexpr float kLeast = -1e30f;
+// A running maximum starts at -inf and is compared as no less than kLeast, the
+// least finite number, so that e^{a - M} is 0 for a = -inf (and NaN for a NaN)
+// without a case of its own.
+constexpr float kLeast = -FLT_MAX;
 HILS_DI float max_of(float a, float b) { return fmaxf(fmaxf(a, b), kLeast); }
 
 // eight elements as float32

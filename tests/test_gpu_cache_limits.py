@@ -1,4 +1,5 @@
-"""The 8-bit paged cache at the ends of its ranges: logits so large that a rounding of theirs is a power of e.
+"""The 8-bit paged cache at the ends of its ranges: logits so large that a rounding of theirs is a power of e, and so
+far below zero that sums of weights must not be taken against a fixed number.
 
 Tolerances are those of test_gpu_cache.py.  Where every softmax of a test gives all its mass to one key, with 100 and
 the logits' own errors between it and the next, an error of a logit moves no weight by more than e^-100, so that
@@ -95,3 +96,30 @@ def test_summaries_at_logits_of_ten_thousands_and_more(dtype, code, G, times):
     assert out_off(dtype, k_sum[0], want, mag, low, weights_off(dtype, code, 128, S, S, 0, 0)) <= 0
     # the one weight's exponent is 0: log and exp of 1, to 2^-20 each
     assert (b_sum[0].double().cpu() - ent).abs().max() <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype,code,G", [(BF, I8, 4), (BF, E4, 2), (F32, I8, 2), (F32, E4, 8)])
+def test_attention_where_every_logit_is_far_below_zero(dtype, code, G):
+    """A window of logits below -1e30 (in codes, in the tail, in both): the largest still takes the mass."""
+    S = 64
+    lens = [S, 2 * S, 20, S + 9, 2 * S]
+    B = len(lens)
+    c = Case(B, G, 1, 128, S, 8 * S, dtype, code, W=2 * S, K=2)
+    axis = torch.randint(0, 2, (128,), generator=c.gen).float() * 2 - 1
+    n = sum(lens)
+    y = torch.empty(n).uniform_(0.5, 1.0, generator=c.gen)
+    for a, L in zip([sum(lens[:b]) for b in range(B)], lens):
+        y[a + int(torch.randint(L, (1,), generator=c.gen))] = 0.25
+    k = (-2.0 ** 55 * y[:, None, None] * axis).to(dtype)
+    q = (2.0 ** 55 * torch.empty((B, G, 1)).uniform_(1, 2, generator=c.gen) * axis).to(dtype)
+    c.append(lens, lens, k, c.rand(n, 1, 128))
+    idx = torch.full((B, 1, 2), -1, dtype=torch.int32)
+    s_sel = torch.full((B, G, 2), -math.inf)
+    out = torch.full((B, G, 128), 3.0, dtype=dtype, device=DEV)
+    H.hils_attn_decode_cache(c.cfg, q.to(DEV), c.paged(lens), c.cache, idx.to(DEV), s_sel.to(DEV), out)
+    H.hils_sync_status()
+    for b, L in enumerate(lens):
+        want, mag, low, big, _ = attend(q[b].double(), c.ref.values(0, b, L), c.ref.values(1, b, L), idx[b].tolist(),
+                                        s_sel[b].double(), S, c.W, c.scale)
+        assert big > 1e31 and want.isfinite().all()
+        assert out_off(dtype, out[b], want, mag, low, weights_off(dtype, code, 128, S, 2 * S, 0, 0)) <= 0, b
