@@ -752,6 +752,20 @@ static hils_status_t cache_args(const hils_config_t* cfg, const hils_paged_t* pa
   return cache_view(*s, cache, cv);
 }
 
+// whether the d elements at i x + j y, i < nx, j < ny, are other ones for each (i, j)
+static bool apart(int64_t nx, int64_t x, int64_t ny, int64_t y, int64_t d) {
+  if ((nx > 1 && x < d) || (ny > 1 && y < d)) return false;
+  if (nx == 1 || ny == 1 || x / ny >= y) return true;  // (rows of heads)
+  for (int64_t j = 1; j < ny; ++j) {  // j y between two multiples of x
+    const __int128 at = (__int128)j * y;
+    for (__int128 i = at / x; i <= at / x + 1; ++i) {
+      const __int128 gap = at - i * x;
+      if (i >= 1 && i < nx && gap < d && gap > -d) return false;
+    }
+  }
+  return true;
+}
+
 hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* paged, const hils_cache_t* cache,
                                 const hils_rows_t* rows, const hils_rope_t* rope, void* stream) {
   HILS_NVTX;
@@ -779,8 +793,8 @@ hils_status_t hils_cache_append(const hils_config_t* cfg, const hils_paged_t* pa
                     (long long)st[i]);
     if (rows->q == rows->q_out && rows->q && (st[4] != st[6] || st[5] != st[7]))
       return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: q_out in place needs the strides of q");
-    // written rows: one address, one element (rows of heads or heads of rows)
-    if (rows->q && !((st[7] >= s.d || s.Hq == 1) && (st[6] >= s.d || rows->n_rows == 1)))
+    // written rows: one address, one element
+    if (rows->q && !apart(rows->n_rows, st[6], s.Hq, st[7], s.d))
       return fail(HILS_ERR_INVALID_ARG, "hils_cache_append: rows or heads of q_out lie on one another (strides %lld, "
                                         "%lld, d=%d)",
                   (long long)st[6], (long long)st[7], s.d);

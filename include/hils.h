@@ -340,9 +340,8 @@ typedef struct {
  * elements, from one row / one head to the next (multiples of 16 bytes; the d
  * elements of a head are contiguous), so that k, v and q may be views of one
  * projection's output.  q may be NULL; else its rotated rows go to q_out, which
- * may be q itself with the same strides and overlaps nothing otherwise; its
- * own rows and heads lie apart (strides of at least d, those of k, v and q may
- * be 0). */
+ * may be q itself with the same strides and overlaps nothing otherwise.  Its
+ * rows and heads share no element; the strides of k, v and q may be 0. */
 typedef struct {
   const void* k;            /* [n_rows, Hkv, d] dtype */
   const void* v;            /* [n_rows, Hkv, d] */

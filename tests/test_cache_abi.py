@@ -127,6 +127,28 @@ def test_outputs_that_lie_on_one_another_are_refused():
     assert b"same memory" in H.load().hils_last_error()
 
 
+@pytest.mark.parametrize("n,Hq,row,head", [(10, 8, 128, 128), (10, 8, 256, 128), (10, 8, 896, 128), (10, 8, 1016, 128),
+                                           (10, 8, 128, 1264), (10, 8, 136, 1344), (3, 8, 384, 256), (2, 2, 128, 128),
+                                           (2 ** 31 - 1, 8, 128, 2 ** 37), (10, 2, 2 ** 62, 2 ** 62)])
+def test_rows_of_q_out_that_lie_between_heads_are_refused(n, Hq, row, head):
+    """Strides of at least d that give two rows' heads elements in common."""
+    apart = H.Cache(P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, H.HILS_KV_I8)
+    assert call("append", config(Hq=Hq, Hkv=1), cache=apart, rows=rows(n_rows=n, q_out_row=row, q_out_head=head)) == INVALID
+    assert b"q_out lie on one another" in H.load().hils_last_error()
+
+
+@pytest.mark.parametrize("n,Hq,row,head", [(10, 8, 1024, 128), (10, 8, 128, 1280), (10, 8, 1152, 144), (10, 8, 2048, 136),
+                                           (10, 8, 1080, 136), (1, 8, 0, 128), (10, 1, 128, 0), (1, 1, 0, 0),
+                                           (2 ** 31 - 1, 8, 128, 2 ** 38), (2, 2, 2 ** 62, 2 ** 61),
+                                           (2, 8, 384, 256), (2, 8, 640, 256), (4, 4, 384, 896)])
+def test_rows_of_q_out_that_lie_apart_are_taken(n, Hq, row, head):
+    """Rows of heads and heads of rows, packed or not, and others that meet nowhere (the call is refused further on: the cache's memory is shared)."""
+    c = config(Hq=Hq, Hkv=1)
+    shared = H.Cache(P, P, P, P, P, P, H.HILS_KV_I8)
+    assert call("append", c, cache=shared, rows=rows(n_rows=n, q_out_row=row, q_out_head=head)) == INVALID
+    assert b"share memory" in H.load().hils_last_error()
+
+
 def test_rope_tables():
     """cos and sin of p base^(-2 i / rot) rounded once to float32, also at far positions."""
     cos, sin = H.rope_tables(200000, 32, base=500000.0, device="cpu")
