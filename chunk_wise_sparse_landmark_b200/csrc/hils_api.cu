@@ -755,7 +755,7 @@ static hils_status_t cache_args(const hils_config_t* cfg, const hils_paged_t* pa
 // whether the d elements at i x + j y, i < nx, j < ny, are other ones for each (i, j)
 static bool apart(int64_t nx, int64_t x, int64_t ny, int64_t y, int64_t d) {
   if ((nx > 1 && x < d) || (ny > 1 && y < d)) return false;
-  if (nx == 1 || ny == 1 || x / ny >= y) return true;  // (rows of heads)
+  if (nx == 1 || ny == 1 || x / ny >= y || y / nx >= x) return true;  // rows of heads, heads of rows
   for (int64_t j = 1; j < ny; ++j) {  // j y between two multiples of x
     const __int128 at = (__int128)j * y;
     for (__int128 i = at / x; i <= at / x + 1; ++i) {
