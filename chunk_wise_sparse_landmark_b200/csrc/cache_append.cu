@@ -182,6 +182,22 @@ HILS_DI bool seq_rows(const NewRows& nr, int b, int& r0, int& r1) {
   r1 = row_begin(nr, b + 1);
   return r0 >= 0 && r1 >= r0 && r1 <= nr.n_rows;
 }
+constexpr int kNobody = 0x7fffffff;
+// Whether one of the sequences tid, tid + kThreads .. before b ends behind b's
+// first row.  (row_start falls somewhere then; the rows that two sequences name
+// are those of the earlier one.)  These loops over sequences are not unrolled: a
+// launch fetches its code anew, and a decode step of 16 sequences took 32.8 us for
+// 31.8 with them unrolled.
+HILS_DI bool begins_inside(const NewRows& nr, int b, int tid) {
+  const int first = row_begin(nr, b);
+  bool inside = false;
+#pragma unroll 1
+  for (int x = tid; x < b; x += kThreads) {
+    int r0, r1;
+    inside = inside || (seq_rows(nr, x, r0, r1) && r1 > first);
+  }
+  return inside;
+}
 HILS_DI bool len_fits(const Shape& s, int L, int n) { return L >= 1 && L <= s.N && n <= L; }
 
 // the angle row of new row r at cache position p, or -1 (reported)
@@ -215,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
   constexpr int SLOTS = D / 16;  // two groups of eight elements each
   constexpr int STEP = kThreads / SLOTS, NI = (S + STEP - 1) / STEP;  // rows of a pass, passes over a chunk
   constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;  // heads that a thread of the queries' part has in flight
-  __shared__ int sh_b;
+  __shared__ int sh_b, sh_falls;  // whether row_start falls somewhere
   __shared__ int sh_seq[kThreads / 2];
+  __shared__ int sh_inside[kThreads / 2];
   __shared__ unsigned sh_top[2][kThreads / 32];
   const unsigned long long zero = grid_begin();
   behind(zero, cv), behind(zero, dv), behind(zero, nr), behind(zero, rp);
@@ -247,15 +264,36 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
       }
     };
     ask(h0);
-    if (tid < rows) sh_seq[tid] = -1;
+    if (tid < rows) sh_seq[tid] = kNobody;
+    if (tid == 0) sh_falls = 0;
     __syncthreads();
+#pragma unroll 1
     for (int b = tid; b < s.B; b += kThreads) {
       int a, z;
-      if (!seq_rows(nr, b, a, z)) continue;
+      const bool fine = seq_rows(nr, b, a, z);
+      if (z < a) sh_falls = 1;
+      if (!fine) continue;
+#pragma unroll 1
       for (int y = max(a, t0); y < min(z, t0 + rows); ++y) sh_seq[y - t0] = b;
     }
     __syncthreads();
-    if (!live || sh_seq[i] < 0) return;
+    if (__builtin_expect(sh_falls, 0)) {  // a row may have several: the first of them, if it begins inside no other
+      if (tid < rows) sh_inside[tid] = 0;
+#pragma unroll 1
+      for (int b = tid; b < s.B; b += kThreads) {
+        int a, z;
+        if (!seq_rows(nr, b, a, z)) continue;
+#pragma unroll 1
+        for (int y = max(a, t0); y < min(z, t0 + rows); ++y) atomicMin(&sh_seq[y - t0], b);
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int y = 0; y < rows; ++y)
+        if (sh_seq[y] != kNobody && begins_inside(nr, sh_seq[y], tid)) sh_inside[y] = 1;
+      __syncthreads();
+      if (live && sh_inside[i]) return;
+    }
+    if (!live || sh_seq[i] == kNobody) return;
     const int b = sh_seq[i], a = row_begin(nr, b), z = row_begin(nr, b + 1);
     const int L = dv_len(dv, s, b);
     if (!len_fits(s, L, z - a)) return;  // reported by the cache's part
@@ -284,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
 
   // ---- cache: (unit, KV head), keys and values.  Sequence b owns the units from
   // row_start[b] / S + 2 b on: floor(n / S) + 2 of them at least, and n rows
-  // touch no more chunks than that.
+  // touch no more chunks than that.  (Sequences that share units share rows.)
   const int g = cta % s.Hkv, u = cta / s.Hkv;
   int b = -1;
   if (!nr.row_start) {
@@ -292,19 +330,31 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(
     if (b >= s.B || u >= (b + 1) / S + 2 * b + 2 || u < b / S + 2 * b) b = -1;
   }
   if (b < 0) {
-    if (tid == 0) sh_b = -1;
+    if (tid == 0) sh_b = kNobody, sh_falls = 0;
     __syncthreads();
+#pragma unroll 1
     for (int x = tid; x < s.B; x += kThreads) {
       int r0, r1;
-      if (!seq_rows(nr, x, r0, r1)) {
+      const bool fine = seq_rows(nr, x, r0, r1);
+      if (r1 < r0) sh_falls = 1;
+      if (!fine) {
         if (cta == 0) raise_status(ctx, kStatusBadIndex);
         continue;
       }
       if (u >= r0 / S + 2 * x && u < r1 / S + 2 * x + 2) sh_b = x;
     }
     __syncthreads();
+    if (__builtin_expect(sh_falls, 0)) {  // the unit may be several sequences': the first one's, if it begins inside no other
+#pragma unroll 1
+      for (int x = tid; x < s.B; x += kThreads) {
+        int r0, r1;
+        if (seq_rows(nr, x, r0, r1) && u >= r0 / S + 2 * x && u < r1 / S + 2 * x + 2) atomicMin(&sh_b, x);
+      }
+      __syncthreads();
+      if (sh_b == kNobody || __syncthreads_or(begins_inside(nr, sh_b, tid))) return;
+    }
     b = sh_b;
-    if (b < 0) return;
+    if (b == kNobody) return;
   }
   const int r0 = row_begin(nr, b), n = row_begin(nr, b + 1) - r0;
   if (n == 0) return;

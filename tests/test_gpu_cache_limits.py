@@ -11,8 +11,8 @@ import pytest
 import torch
 
 from chunk_wise_sparse_landmark_b200 import hils as H
-from tests.cache_ref import attend, summaries
-from tests.test_gpu_cache import BF, DEV, E4, F32, FIXED_Q, I8, Case, out_off, weights_off
+from tests.cache_ref import attend, rotate, summaries
+from tests.test_gpu_cache import BF, DEV, E4, F32, FIXED_Q, I8, Case, expect_bad, out_off, same, weights_off
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,51 @@ def test_attention_where_every_logit_is_far_below_zero(dtype, code, G):
                                         s_sel[b].double(), S, c.W, c.scale)
         assert big > 1e31 and want.isfinite().all()
         assert out_off(dtype, out[b], want, mag, low, weights_off(dtype, code, 128, S, 2 * S, 0, 0)) <= 0, b
+
+
+def sequences_taken(start, n_rows):
+    """[first, end) of the sequences whose rows the call takes: in [0, n_rows), in order, none before an earlier end."""
+    end, taken = 0, []
+    for a, z in zip(start, start[1:]):
+        fine = 0 <= a <= z <= n_rows
+        taken.append((a, z) if fine and a >= end else (0, 0))
+        end = max(end, z) if fine else end
+    return taken
+
+
+def row_starts_out_of_order():
+    gen = torch.Generator().manual_seed(11)
+    many = torch.sort(torch.randint(0, 3000, (701,), generator=gen)).values.tolist()
+    for at in torch.randint(0, 701, (40,), generator=gen).tolist():
+        many[at] += int(torch.randint(-60, 60, (1,), generator=gen))
+    many[100], many[200], many[400], many[500] = 2 ** 31 - 1, -1, 3001, -2 ** 31
+    return {"a fall inside": (1000, [0, 1000, 500, 900]), "a fall to the front": (210, [0, 200, 5, 210]),
+            "taken behind it": (300, [0, 100, 50, 100, 300]), "past the rows": (60, [0, 99999, 20, 40, 60]),
+            "below zero": (40, [-5, 10, 40]), "none taken twice": (256, [0, 128, 64, 192, 128, 256]),
+            "nothing taken": (64, [64, 0]), "700 sequences": (3000, many)}
+
+
+@pytest.mark.parametrize("name", list(row_starts_out_of_order()))
+@pytest.mark.parametrize("dtype,d,S,code", [(F32, 64, 32, I8), (BF, 128, 64, None)], ids=["f32-i8", "bf16-native"])
+def test_row_starts_out_of_order_lose_no_other_sequence(dtype, d, S, code, name):
+    """Each row that two sequences name is the earlier one's; sequences that are skipped are left as they were."""
+    n, start = row_starts_out_of_order()[name]
+    taken = sequences_taken(start, n)
+    B = len(taken)
+    c = Case(B, 4, 2, d, S, 1024 if B < 9 else 256, dtype, code, fill=2.0)
+    assert all(z - a <= c.cap for a, z in taken) and (B < 9 or 300 < sum(z > a for a, z in taken) < 660)
+    angles, rope = c.rope(d, False)
+    k, v, q = c.rand(n, 2, d), c.rand(n, 2, d), c.rand(n, 4, d)
+    lens = [max(1, z - a) for a, z in taken]
+    want = torch.full((n, 4, d), 7.0, dtype=dtype)
+    rows = torch.cat([torch.arange(a, z) for a, z in taken])
+    pos = torch.cat([torch.arange(z - a) for a, z in taken])
+    turn = lambda x: rotate(x, angles[0][pos], angles[1][pos], False)  # noqa: E731
+    want[rows] = turn(q[rows])
+    q_out = torch.full((n, 4, d), 7.0, dtype=dtype, device=DEV)
+    H.hils_cache_append(c.cfg, c.paged(lens), c.cache, k.to(DEV), v.to(DEV), q.to(DEV), q_out, rope,
+                        torch.tensor(start, dtype=torch.int32, device=DEV))
+    expect_bad()
+    c.ref.append(lens, [z - a for a, z in taken], turn(k[rows]), v[rows])
+    c.check()
+    assert same(q_out, want)
