@@ -298,11 +298,18 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
  * are in the tails k_tail / v_tail [B, 2, Hkv, S, d] (cfg->dtype), chunk c in
  * slot c & 1; hils_cache_append also writes the new tokens of the chunk
  * before the last one there.  So what the cache holds does not depend on how
- * the tokens were split over calls, and a sequence may be cut back by the
- * tokens of its last chunk and the one before (its length reduced, other
- * tokens appended) as long as every token of those two chunks was appended
- * here.  A sequence that begins with pages of another one (a shared prefix)
- * begins its own appends at a chunk's first token.  8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
+ * the tokens were split over calls, and a sequence may be cut back (its length
+ * reduced, other tokens appended):
+ *   - to the first token of any chunk;
+ *   - into a chunk c whose tokens below the cut are still in its slot: they were
+ *     appended here, and since the last of those appends no token of chunk c + 2.
+ * The first cut may so go into the last chunk and the one before.  After it, count
+ * from the longest length that the sequence has had: the chunk before that
+ * one's last stays the earliest to be cut into until the sequence has been cut
+ * back to a chunk's first token and appended from there.
+ * A sequence that begins with pages of another one (a shared prefix)
+ * begins its own appends at a chunk's first token.
+ *   8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
  * and dtype BF16 with d = 128, S = 64, and pools of up to 256 GB; native caches every shape of the
  * summaries (hils_attn_decode_cache: those of hils_attn_decode_paged).
  * Pools, tails and scales are 16-byte aligned device memory; scales are >= 0 or
