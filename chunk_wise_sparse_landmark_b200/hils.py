@@ -323,7 +323,9 @@ def _rows(t: torch.Tensor, shape, dtype, at: int):
     return t.data_ptr(), row, head
 
 
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# the current stream and device as numbers: what torch.cuda.current_stream() and current_device() are made of, without
+# an object for each call (a PyTorch without CUDA has neither, and no tensor that a call would take)
+_raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 def _launch(at: int, stream, fn, *args):

@@ -191,3 +191,27 @@ def test_capacities_and_pools_past_the_kernels_ranges():
         assert call(name, config(), pg=H.Paged(P, P, 16, 2 ** 25), rows=rows()) == UNSUPPORTED  # 2^32 lines of 128 bytes
         assert call(name, config(B=65536), rows=rows()) == UNSUPPORTED
         assert call(name, config(Hq=32768, Hkv=32768), rows=rows()) == UNSUPPORTED
+
+
+def test_the_module_is_imported_by_a_pytorch_without_cuda():
+    """The host's checks work where PyTorch has no CUDA functions (they are taken away here)."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+for n in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, n)
+from chunk_wise_sparse_landmark_b200 import hils as H
+cfg = H.make_config(1, 128, 8, 2, 128, 64, 128, 2, torch.bfloat16)
+pool = torch.zeros((4, 2, 64, 128), dtype=torch.bfloat16)
+k = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+try:
+    H.hils_cache_append(cfg, H.Paged(4096, 4096, 2, 4), H.cache(pool, pool), k, k)
+except AssertionError as e:
+    print("refused:", e)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and "refused: the cache is not on a CUDA device" in r.stdout, r.stderr
