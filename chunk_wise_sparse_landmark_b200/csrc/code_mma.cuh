@@ -240,6 +240,7 @@ template <int D, int S, int G>
 struct DigitOps {
   using C = CodeI8;
   static_assert(G <= 4, "one block of columns");
+  static_assert(S % 64 == 0, "a half of the tile is read in whole steps of 32 keys");
   static constexpr int R = 1;  // heads of a thread
   static constexpr float kOne = C::kOne, kLog2One = C::kLog2One;  // weights are given times kOne
   static HILS_DI int head(int, int c4) { return c4; }
