@@ -7,6 +7,7 @@ first call raises (there is no fallback of any kind).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -340,6 +341,11 @@ def _launch(at: int, stream, fn, *args):
         _check(st)
 
 
+def _on(at: int):
+    """A context in which CUDA device `at` is the current one."""
+    return contextlib.nullcontext() if _device() == at else torch.cuda.device(at)
+
+
 def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) -> Cache:
     """A paged cache.  Pools [num_pages, Hkv, S, d] of float32 / bfloat16 (native), int8 or
     float8_e4m3fn (8 bits: with float32 scales [num_pages, Hkv] and tails [B, 2, Hkv, S, d])."""
@@ -618,6 +624,8 @@ class CacheDecode:
 
     def step(self, q, stream=None):
         """Attention of q [B, Hq, d], each sequence's last token (rotated)."""
-        hils_score_topk_paged(self.cfg, q, self.paged, self.k_sum, self.b_sum, self.idx, self.s_sel, self.ws_score, stream)
+        with _on(self.cache.at):  # (the scoring is enqueued on the current device)
+            hils_score_topk_paged(self.cfg, q, self.paged, self.k_sum, self.b_sum, self.idx, self.s_sel, self.ws_score,
+                                  stream)
         hils_attn_decode_cache(self.cfg, q, self.paged, self.cache, self.idx, self.s_sel, self.out, self.ws_attn, stream)
         return self.out

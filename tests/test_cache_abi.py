@@ -215,3 +215,41 @@ except AssertionError as e:
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0 and "refused: the cache is not on a CUDA device" in r.stdout, r.stderr
+
+
+class FakeDevices:
+    """Two CUDA devices that are only counted: what torch.cuda.device makes current."""
+
+    def __init__(self, monkeypatch):
+        self.now = 0
+        monkeypatch.setattr(H, "_device", lambda: self.now)
+        monkeypatch.setattr(H, "_raw_stream", lambda at: 100 + at)
+        monkeypatch.setattr(torch.cuda, "device", self.device)
+
+    def device(self, at):
+        import contextlib
+
+        @contextlib.contextmanager
+        def current():
+            old, self.now = self.now, at
+            try:
+                yield
+            finally:
+                self.now = old
+
+        return current()
+
+
+def test_a_decode_step_is_enqueued_on_the_device_of_its_cache(monkeypatch):
+    devices, seen = FakeDevices(monkeypatch), []
+    monkeypatch.setattr(H, "hils_score_topk_paged", lambda *a: seen.append(("score", devices.now, a[-1])))
+    monkeypatch.setattr(H, "hils_attn_decode_cache",
+                        lambda *a: H._launch(dec.cache.at, a[-1], lambda raw: seen.append(("attn", devices.now, raw))))
+    dec = H.CacheDecode.__new__(H.CacheDecode)
+    dec.cfg, dec.paged, dec.cache = config(), H.Paged(P, P, 16, 100), H.Cache(**OK)
+    dec.k_sum = dec.b_sum = dec.idx = dec.s_sel = dec.ws_score = dec.out = dec.ws_attn = None
+    for at in (1, 0):
+        dec.cache.at = at
+        dec.step(None)
+        assert seen == [("score", at, None), ("attn", at, 100 + at)] and devices.now == 0
+        seen.clear()
