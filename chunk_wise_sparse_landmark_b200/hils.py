@@ -91,7 +91,7 @@ class Paged(ctypes.Structure):
         ("max_pages", ctypes.c_int32),
         ("num_pages", ctypes.c_int32),
     ]
-    batch = None  # sequences of the tables, where known (paged())
+    batch = at = None  # sequences and CUDA device of the tables, where known (paged())
 
 
 class Cache(ctypes.Structure):
@@ -270,9 +270,10 @@ def hils_prefill_bwd(cfg: Config, q, k, v, q_lmk, idx, s_sel, k_sum, dout, dq, d
 def paged(seq_lens, block_table, num_pages: int) -> Paged:
     """seq_lens [B] and block_table [B, max_pages] are int32 CUDA tensors."""
     assert seq_lens.dtype == torch.int32 and block_table.dtype == torch.int32
+    assert seq_lens.get_device() == block_table.get_device(), "the lengths and the page table are on different devices"
     pg = Paged(_p(seq_lens).value, _p(block_table).value, block_table.shape[1], num_pages)
     pg.tensors = (seq_lens, block_table)  # the description keeps what it points to
-    pg.batch = min(seq_lens.shape[0], block_table.shape[0])
+    pg.batch, pg.at = min(seq_lens.shape[0], block_table.shape[0]), seq_lens.get_device()
     return pg
 
 
@@ -376,6 +377,7 @@ def cache(k_pool, v_pool, k_scale=None, v_scale=None, k_tail=None, v_tail=None) 
 
 def _cache_fits(cfg: Config, pg: Paged, c: Cache):
     assert c.at >= 0, "the cache is not on a CUDA device"
+    assert pg.at in (None, c.at), "the page table is on another device than the cache"
     assert c.tile == (cfg.n_kv_heads, cfg.chunk, cfg.head_dim) and c.elements is _dtype(cfg) and (
         pg.num_pages <= c.pages and c.sequences in (None, cfg.batch) and pg.batch in (None, cfg.batch)), "the cache does not fit the configuration or its page table"
 

@@ -253,3 +253,22 @@ def test_a_decode_step_is_enqueued_on_the_device_of_its_cache(monkeypatch):
         dec.step(None)
         assert seen == [("score", at, None), ("attn", at, 100 + at)] and devices.now == 0
         seen.clear()
+
+
+def test_a_page_table_on_another_device_than_its_cache_is_refused(monkeypatch):
+    """Kernels would read its addresses on the cache's device (devices are only counted here)."""
+    FakeDevices(monkeypatch)
+    monkeypatch.setattr(H, "_p", lambda t: ctypes.c_void_p(P))
+    pg = H.paged(torch.zeros(2, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32), 4)
+    assert pg.batch == 2 and pg.at == -1
+    pool, scale = torch.zeros((4, 2, 64, 128), dtype=torch.int8), torch.zeros((4, 2))
+    tail = torch.zeros((2, 2, 2, 64, 128), dtype=torch.bfloat16)
+    c = H.cache(pool, pool, scale, scale, tail, tail)
+    c.at, pg.at = 0, 1
+    cfg, k = config(N=128), torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    idx, s_sel, q = torch.zeros((2, 2, 4), dtype=torch.int32), torch.zeros((2, 8, 4)), torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    for run in (lambda: H.hils_cache_append(cfg, pg, c, k, k), lambda: H.hils_cache_read(cfg, pg, c, k[None], k[None]),
+                lambda: H.hils_build_summaries_cache(cfg, pg, c, q, q, s_sel),
+                lambda: H.hils_attn_decode_cache(cfg, q, pg, c, idx, s_sel, q)):
+        with pytest.raises(AssertionError, match="page table is on another device"):
+            run()
