@@ -16,9 +16,10 @@
 // load and store.  The other rotates rows of the queries.  Both read each element
 // once and write it once.  Alone, the first is bound by its instructions and
 // waits (scale, then codes), the second by the memory, so they are mixed: 32768
-// rows, 32 heads over 8, int8: 141 us, 5.4 TB/s of the 755 MB it must move; the
-// kinds one after the other 156; the first kind alone 70 us (2.9 TB/s).  8192 rows
-// into bf16 pages: 36.1 us, 5.7 TB/s.  48 single float32 rows: 3.6 us.
+// rows, 32 heads over 8, int8: 138 us, 5.5 TB/s of the 755 MB it must move (an
+// earlier form 141: the kinds one after the other 156, the first kind alone 70 us,
+// 2.9 TB/s).  8192 rows into bf16 pages: 35.0 us, 5.9 TB/s; into float32 pages 69.7
+// us, 5.8 TB/s.  48 single float32 rows: 3.6 us.
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -499,7 +500,11 @@ cudaError_t go_append(const Shape& s, const CacheView& cv, const DecView& dv, co
   constexpr int SLOTS = D / 16;
   const long long kv = ((long long)nr.n_rows / S + 2ll * s.B) * s.Hkv;
   // lanes of a row: all heads at once for few rows (latency); a quarter (float32:
-  // half) of them for many, so that one load of the angles serves several heads
+  // half) of them for many, so that one load of the angles serves several heads.
+  // 32 heads over 8, us, all : part.  bf16 pages, d = 128: 16 rows 3.2 : 3.3, 256
+  // 5.0 : 4.6, 1024 9.1 : 7.0, 2048 14.9 : 11.0, 16384 103 : 70.  float32, d = 64:
+  // 256 4.9 : 5.4, 1024 8.1 : 9.1, 2048 13.0 : 13.4, 4096 23.6 : 23.7, 16384 90 : 80.
+  // So 2048 is float32's border; from 64 to 2047 bf16 rows part would be shorter.
   constexpr int per = sizeof(T) == 2 ? 4 : 2;
   int lanes = s.Hq < kThreads / SLOTS ? s.Hq : kThreads / SLOTS;
   if (nr.n_rows >= 2048) lanes = (lanes + per - 1) / per;
@@ -549,7 +554,7 @@ HILS_DI void store16(__nv_bfloat16* p, const float (&x)[16], bool wide) {
 
 // One CTA per (chunk, KV head, sequence; keys or values): a tile is contiguous
 // in the pool and in the output.  Bound by memory: 32768 rows, 8 heads, int8 to
-// bf16: 33.6 us, 6.0 TB/s.
+// bf16: 34.0 us, 5.9 TB/s.
 template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(Shape s, CacheView cv, DecView dv, T* __restrict__ k_out,
                                                               T* __restrict__ v_out, int out_rows, DevCtx ctx) {

@@ -20,7 +20,10 @@ namespace {
 constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------------------
-// Native caches: the summaries on CUDA cores, one CTA for a chunk at a time.
+// Native caches: the summaries on CUDA cores, one CTA for a chunk at a time: 131072
+// tokens, 32 heads over 8, bf16: 300 us for a floor of 46; 32768 in float32, d = 64,
+// 16 heads over 4: 23 us for 6.4 (hils_build_summaries_paged: 299, 25).  Far from
+// the memory's rate: scalar products out of shared memory, two-byte loads.
 template <typename T, int D, int S, int G>
 __global__ void __launch_bounds__(kThreads) native_summaries_kernel(Shape s, CacheView cv, DecView dv,
                                                                    const T* __restrict__ q_lmk, LmkStrides ls,
@@ -178,15 +181,16 @@ HILS_DI float lift(float scale, float (&o)[R][N]) {
 // Warps take the chunks of all sequences in turn, so that short and long
 // sequences share the work evenly.  A CTA serves sequences [kSeqs blockIdx.y, +
 // kSeqs): their numbers of chunks are summed up in shared memory, and unit u is
-// KV head u % Hkv of chunk u / Hkv of that order.  Computing bounds it (about 1000
-// instructions of a warp for a tile of 8 KB; without its tile copies it takes as
-// long), so that many warps matter: a warp has three half tiles of buffer, 12 KB,
-// and sixteen warps share a multiprocessor (two whole tiles and twelve warps: 39.6
-// us instead of 35.2).  It holds a tile and the first half of the next one, whose
+// KV head u % Hkv of chunk u / Hkv of that order.  The latency of a warp's own chain
+// bounds it, about 1100 instructions for a tile of 8 KB, most of them waiting for one
+// just before (issue slots 53% used, ALU pipe 50%, tensor pipe 24%; without its tile copies it
+// takes as long), so that many warps matter: a warp has three half tiles of buffer,
+// 12 KB, and sixteen warps share a multiprocessor (two whole tiles and twelve warps:
+// 39.6 us instead of 35.2).  It holds a tile and the first half of the next one, whose
 // second half takes the place of this one's first half once that has been read.
 // The landmark rows of the next unit are asked for before this one is computed.
-// 131072 tokens, 32 heads over 8, e4m3: 35.2 us, 4.8 TB/s of the 168 MB it must move;
-// 55K tokens in 13 sequences, 16 heads over 8, int8: 18.0 us, 3.5 TB/s.
+// 131072 tokens, 32 heads over 8, e4m3: 34.8 us, 4.8 TB/s of the 168 MB it must move;
+// 55K tokens in 13 sequences, 16 heads over 8, int8: 17.7 us, 3.6 TB/s.
 constexpr int kSeqs = 512;
 template <typename T>
 constexpr int summary_ctas() { return sizeof(T) == 2 ? 4 : 3; }  // of a multiprocessor
@@ -430,7 +434,7 @@ HILS_DI void row8(const float* p, float (&x)[8]) {
 // gq + 8 x and head Ops::head(r, c4), and acc += weights . values (dims gq D / 8 + x).
 // float32 configurations: on CUDA cores, eight keys, so that a tail is shared by more
 // warps, and a quarter of a key's dims to a thread (24 sequences of 4K, d = 64, S = 32,
-// G = 4: 7.4 us; sixteen keys 10.3; eight, a key's dims and two heads to a thread 7.9).
+// G = 4: 7.5 us; sixteen keys 10.3; eight, a key's dims and two heads to a thread 7.9).
 template <typename T, typename Ops, int D>
 struct TailSlice {
   static constexpr int R = Ops::R, N8 = D / 8, KEYS = 8;
@@ -577,9 +581,9 @@ constexpr size_t attn_smem(int nwarp, int ncta) {
 // values; the next unit's keys are asked for when this one's scores are done, its
 // values when this one's sums are.
 // Bound by memory where there are many sequences: 64 of 16K, K = 32, W = 512, 32 heads
-// over 8, int8: 57.7 us, 5.8 TB/s; 256: 198 us, 6.8 TB/s; 16: 18.9 us, 4.4 TB/s, of
+// over 8, int8: 57.9 us, 5.8 TB/s; 256: 199 us, 6.8 TB/s; 16: 18.9 us, 4.4 TB/s, of
 // which the launch, three dependent loads, the first tile's way and the folds are
-// about 6.  One sequence, K = 16: 6.5 us, half of it those.
+// about 6.  One sequence, K = 16: 6.6 us, half of it those.
 template <typename T, typename C, int D, int S, int G>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) attn_codes_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Shape s,

@@ -14,6 +14,11 @@
 //   are computed times 2^15 for the same reason: within 2^-11 of themselves, or
 //   2^-40 of the largest.  PARTS = 2 (float32 configurations) holds queries and
 //   weights as a sum of two halves (the nearest one and the rest): within 2^-22.
+//   bf16 configurations take one half of a weight: their results round to bf16, 2^-8
+//   of themselves, and over e4m3 codes are off by 1.665e-3 (2-norm, against 64
+//   bits) where plain 32-bit arithmetic is by 1.657e-3.  A second half makes it
+//   1.657e-3 and takes 7% longer (attention, 96 x 16K: 84.3 -> 90.4 us), 15% for
+//   summaries (128K tokens: 37.1 -> 42.7).
 // * DigitOps (int8 codes, bf16, up to four heads): 8-bit m16n8k32 with int32 sums
 //   on the codes as they are.  A query or weight is a fixed-point number in 8-bit
 //   digits, each a column of its own: three for a query (within 2^-24 of its

@@ -307,6 +307,7 @@ hils_status_t hils_attn_decode_paged(const hils_config_t* cfg, const void* q, co
  * from the longest length that the sequence has had: the chunk before that
  * one's last stays the earliest to be cut into until the sequence has been cut
  * back to a chunk's first token and appended from there.
+ * A sequence that moves to another row of the batch takes its tails along.
  * A sequence that begins with pages of another one (a shared prefix)
  * begins its own appends at a chunk's first token.
  *   8-bit formats serve dtype F32 with d in {64, 128}, S in {32, 64},
