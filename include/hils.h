@@ -365,9 +365,10 @@ typedef struct {
  * the cache (one launch; paged->seq_lens already counts the new tokens).
  *   rope: NULL leaves q and k as they are (q is then copied to q_out).
  * Checked on the device and reported as for hils_decode_append: a sequence
- * with new rows whose rows do not lie in [0, n_rows) in order, or begin before
- * the end of an earlier sequence's that do, whose length is
- * outside [1, L_max] or below its number of new rows is skipped; a page outside
+ * with new rows is skipped if those do not lie in [0, n_rows) in order, if they
+ * begin before the end of an earlier sequence's rows (which lie in order
+ * themselves), or if its length is outside [1, L_max] or below its number of
+ * new rows; the others are appended.  A page outside
  * the pool is not written; a row whose position lies outside the tables is
  * stored unrotated.  Rows of no sequence (before row_start[0], from
  * row_start[B] on) are never written.  No page may belong to two
